@@ -240,6 +240,108 @@ smla_status sparse_mla_bwd(const void* q, const void* kv, const void* out, const
                            const float* lse, float sm_scale, int d_v, float* dq, float* dkv, float* dsink,
                            int64_t s_q, int64_t s_kv, int h_q, int d_qk, int topk, smla_stream_t stream);
 
+/*
+ * Page planning of one serving step, on the device: which cache pages and rows the step's new
+ * tokens get, from the requests' lengths alone.  For request b, with o_b = max(seqlens[b], 0)
+ * cached and m_b = max(new_lens[b], 0) new tokens:
+ *   cu_seqlens_q  [n_req + 1]  running sums of m_b from 0, clamped to n_tokens; c_b is the
+ *                              difference of entries b + 1 and b
+ *   seqlens_k     [n_req]      o_b + c_b
+ *   block_table   [n_req, max_blocks]  columns ceil(o_b / page_block) .. ceil(seqlens_k[b] /
+ *                              page_block) - 1 (those below max_blocks) get the next pages of
+ *                              the free list, request by request and column by column, -1 once
+ *                              the list is used up; every other column is left as it is
+ *   positions     [n_tokens]   o_b + t - cu_seqlens_q[b] for token t of request b, -1 behind
+ *                              the last token
+ *   slots         [n_tokens]   table entry of the position * page_block + position % page_block;
+ *                              -1 behind the last token, past the table's last column, or where
+ *                              the entry is negative
+ *   counts        [3]          tokens placed, index of the first free page not handed out,
+ *                              pages that were needed but not there
+ *   free_pages    [n_free]     page ids; the pages are handed out from index free_start[0]
+ *                              (device memory, NULL: 0; negative: 0).  The previous step's
+ *                              counts + 1 is a valid free_start, in another buffer.
+ * The block table, the lengths and the sums have the layouts that sparse_mla_fwd_paged,
+ * sparse_mla_append_kv and sparse_mla_chunk_fwd_paged read.  With the same inputs a second call
+ * writes the same values.  n_tokens may exceed the step's tokens (a padded batch).  Sizes are
+ * at least 0; max_blocks and page_block at least 1, their product, n_tokens, n_free and every
+ * o_b + c_b at most INT32_MAX.  Pointers are 4-byte aligned; those of empty arrays may be
+ * NULL.  SMLA_ERR_BAD_SHAPE when an output overlaps an input or another output.
+ */
+smla_status sparse_mla_plan_pages(const int32_t* seqlens, const int32_t* new_lens, int32_t* block_table,
+                                  const int32_t* free_pages, const int32_t* free_start, int32_t* seqlens_k,
+                                  int32_t* cu_seqlens_q, int32_t* slots, int32_t* positions, int32_t* counts,
+                                  int64_t n_req, int64_t n_free, int64_t n_tokens, int max_blocks, int page_block,
+                                  smla_stream_t stream);
+
+/*
+ * Appends the latent rows of n new tokens to a paged cache, and turns the queries' rotary columns
+ * in the same launch.  Row slots[t] of kv_pool becomes
+ *   [0, 512)    c_kv[t, d] * norm_weight[d] / sqrt(mean(c_kv[t]^2) + eps), or c_kv[t] as it is
+ *               when norm_weight is NULL
+ *   [512, 576)  (d_qk 576 only) k_pe[t] with each pair (x, y) of columns 2i, 2i + 1 turned to
+ *               (x cos - y sin, y cos + x sin); as it is when rope is NULL
+ * and, when q_pe is given, q[t, h, 512:] becomes q_pe[t, h] turned by the same angles.
+ *   c_kv         [n, 512] bf16, row stride c_stride elements (a multiple of 8), 16-byte aligned
+ *   k_pe         [n, 64] bf16, row stride k_stride (even), 4-byte aligned; given exactly when
+ *                d_qk is 576
+ *   slots        [n] int32 pool rows; a negative one, or one >= pool_rows, is not written
+ *   positions    [n] int32 rows of the rope table (with rope only)
+ *   rope         [max_pos, 64] fp32, 16-byte aligned: 32 cosines, then 32 sines of a position; NULL
+ *                for none.  A token whose position lies outside [0, max_pos) is padding: neither
+ *                its cache row nor its q columns are written.
+ *   norm_weight  [512] bf16, 16-byte aligned, or NULL; eps finite and >= 0
+ *   q_pe         [n, h_q, 64] bf16, strides q_stride_t and q_stride_h elements (multiples of 8),
+ *                16-byte aligned, or NULL; needs rope.  It may be q[..., 512:] itself.
+ *   q            [n, h_q, 576] bf16, 16-byte aligned; given exactly when q_pe is
+ *   kv_pool      [pool_rows, d_qk] bf16, 16-byte aligned
+ * Arithmetic is fp32, each value is rounded to bf16 once; without a norm weight (without rope) the
+ * bits are copied.  Two tokens with one slot leave that row undefined.  kv_pool must not overlap
+ * c_kv or k_pe (SMLA_ERR_BAD_SHAPE).  n == 0 is a no-op.
+ */
+smla_status sparse_mla_append_kv(const void* c_kv, int64_t c_stride, const void* k_pe, int64_t k_stride,
+                                 const int32_t* slots, const int32_t* positions, const float* rope, int64_t max_pos,
+                                 const void* norm_weight, float eps, const void* q_pe, int64_t q_stride_t,
+                                 int64_t q_stride_h, void* q, int h_q, void* kv_pool, int64_t pool_rows, int d_qk,
+                                 int64_t n, smla_stream_t stream);
+
+/*
+ * Dense attention of a chunk of new tokens over a paged latent cache: the operation of
+ * sparse_mla_fwd_paged with every visible position counted instead of an index list, for ragged
+ * requests of one token (decode) to whole prompts (chunked prefill).
+ *   q             [n_tok, h_q, d_qk] bf16; rows cu_seqlens_q[b] .. cu_seqlens_q[b + 1] - 1 are
+ *                 request b's q_b new tokens (values are clamped to [0, n_tok]; they must not
+ *                 decrease).  Rows of no request are left unwritten in every output.
+ *   kv_pool       [pool_rows, 1, d_qk] bf16
+ *   block_table   [n_req, max_blocks] int32, as in sparse_mla_fwd_paged
+ *   seqlens_k     [n_req] int32: keys of request b, its new tokens' own rows among them
+ *   causal        nonzero: token i of request b (at position seqlens_k[b] - q_b + i) sees the
+ *                 positions up to its own; zero: it sees every position below seqlens_k[b].  A
+ *                 token at a negative position sees none.
+ *   out, lse, max_logits, attn_sink, sm_scale, d_v: as in sparse_mla_fwd, an empty row's values
+ *                 included (O = 0, lse = +inf, max_logits = -inf)
+ * A position counts only if its page lies in the table's max_blocks columns, the entry is >= 0
+ * and the row is < pool_rows; any other is an invalid slot and never an address.  Rows of
+ * positions at or past seqlens_k[b] are not read into any product: they may hold anything, NaN
+ * among it.  Rows below it must be finite.
+ *   h_q           1 .. 1024 (any: all heads of a token share the one latent row)
+ *   n_tok * h_q   at most INT32_MAX
+ *   workspace     device buffer of at least sparse_mla_chunk_workspace_size(n_tok, h_q) bytes,
+ *                 256-byte aligned, owned by the caller; needs no initialisation, its contents
+ *                 are meaningless after the call.  Two calls in flight at once must not share it.
+ * q, kv_pool and out are 16-byte aligned, the rest 4-byte.  The result does not depend on
+ * anything but the arguments (no atomics): two calls give the same bits.
+ * n_tok == 0 or n_req == 0 is a no-op.
+ */
+size_t sparse_mla_chunk_workspace_size(int64_t n_tok, int h_q);
+
+smla_status sparse_mla_chunk_fwd_paged(const void* q, const void* kv_pool, int64_t pool_rows,
+                                       const int32_t* block_table, int max_blocks, int page_block,
+                                       const int32_t* cu_seqlens_q, const int32_t* seqlens_k, int64_t n_req, int causal,
+                                       const float* attn_sink, float sm_scale, int d_v, void* out, float* lse,
+                                       float* max_logits, int64_t n_tok, int h_q, int d_qk, void* workspace,
+                                       size_t workspace_bytes, smla_stream_t stream);
+
 /* Static, human-readable description of a status code.  Never NULL. */
 const char* sparse_mla_status_string(smla_status status);
 

@@ -15,6 +15,17 @@ O = 0, lse = +inf, max_logits = -inf.
     dq, dkv, dsink = sparse_mla_bwd(q, kv, out, dout, indices, lse, topk_length, attn_sink)
 
 returns the gradients of sum(dout * out) (FlashMLA PR #198, "Summary" item 1) in fp32.
+
+A serving step on the paged cache that :func:`sparse_mla_fwd_paged` reads:
+
+    seqlens_k, cu, slots, positions, counts = sparse_mla_plan_pages(seqlens, new_lens, block_table,
+                                                                    free_pages, n_tokens)
+    sparse_mla_append_kv(c_kv, k_pe, slots, kv_pool, norm_weight, positions=positions, rope=rope,
+                         q_pe=q_pe, q=q)
+    out, lse, max_logits = sparse_mla_chunk_fwd_paged(q, kv_pool, block_table, cu, seqlens_k)
+
+gives the step's tokens their pages and rows, writes the rows, and attends to every cached key (the
+dense form, one token to whole prompts per request).
 """
 from __future__ import annotations
 
@@ -27,7 +38,8 @@ from .native_build import LIB_PATH, build as build_library
 
 __all__ = ["sparse_mla_fwd", "sparse_mla_fwd_paged", "sparse_mla_fwd_paged_splitkv_static", "sparse_mla_fwd_host",
            "row_shard", "sparse_mla_fwd_sharded", "auto_splits",
-           "sparse_mla_bwd", "sparse_mla_device_status",
+           "sparse_mla_bwd", "sparse_mla_plan_pages", "sparse_mla_append_kv", "sparse_mla_chunk_fwd_paged",
+           "sparse_mla_device_status",
            "sparse_mla_status_string", "SmlaError", "load_library", "build_library", "LIB_PATH"]
 
 
@@ -363,6 +375,196 @@ def sparse_mla_bwd(q, kv, out, dout, indices, lse, topk_length=None, attn_sink=N
     if rc != 0:
         raise SmlaError(rc, "sparse_mla_bwd")
     return dq, dkv, dsink
+
+
+def _on_stream(stream, dev, call):
+    """Runs `call` with `stream` as the current one, so that what it allocates belongs to the stream
+    that uses it, and with `dev` as the current device."""
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, the tensors are on {dev}")
+        with torch.cuda.stream(stream):
+            return call()
+    if torch.cuda.current_device() == dev.index:
+        return call()
+    with torch.cuda.device(dev):
+        return call()
+
+
+def _check_shape(t, name, shape):
+    if t is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _check_strided(t, name, shape, dev):
+    """A bf16 tensor of this shape whose last dimension is contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    _check_shape(t, name, shape)
+    if t.numel() and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+
+
+def sparse_mla_plan_pages(seqlens, new_lens, block_table, free_pages, n_tokens, page_block=64, free_start=None,
+                          seqlens_k=None, cu_seqlens_q=None, slots=None, positions=None, counts=None, stream=None):
+    """Pages and rows of one step's new tokens, planned on the device.  seqlens [n_req] and new_lens
+    [n_req] int32: cached and new tokens of each request; block_table [n_req, max_blocks] int32:
+    updated in place with the new pages; free_pages [n_free] int32, handed out from index
+    free_start [1] (int32, None: 0); n_tokens: length of the token arrays, at least the step's
+    tokens (the rest is padding).  Returns int32 tensors (allocated here when not given):
+    seqlens_k [n_req], cu_seqlens_q [n_req + 1], slots [n_tokens] and positions [n_tokens] (-1 for
+    padding; a slot is also -1 where there is no page), counts [3] = tokens placed, next free_start,
+    pages that were missing.  See the C header for the exact rules."""
+    lib = load_library()
+    i32 = torch.int32
+    _check(seqlens, "seqlens", i32)
+    dev = seqlens.device
+    _check(new_lens, "new_lens", i32, dev)
+    _check(block_table, "block_table", i32, dev)
+    _check(free_pages, "free_pages", i32, dev)
+    _check(free_start, "free_start", i32, dev)
+    n_req, n_tokens = seqlens.numel(), int(n_tokens)
+    if n_tokens < 0:
+        raise ValueError("n_tokens must be at least 0")
+    if new_lens.numel() != n_req:
+        raise ValueError("new_lens must have one entry per request")
+    if block_table.dim() != 2 or block_table.shape[0] != n_req:
+        raise ValueError("block_table must be [n_req, max_blocks]")
+    if free_start is not None and free_start.numel() != 1:
+        raise ValueError("free_start must have one entry")
+    given = (("seqlens_k", seqlens_k, n_req), ("cu_seqlens_q", cu_seqlens_q, n_req + 1), ("slots", slots, n_tokens),
+             ("positions", positions, n_tokens), ("counts", counts, 3))
+    for name, t, n in given:
+        _check(t, name, i32, dev)
+        _check_shape(t, name, (n,))
+
+    def call():
+        outs = [torch.empty(n, dtype=i32, device=dev) if t is None else t for _, t, n in given]
+        rc = lib.sparse_mla_plan_pages(
+            seqlens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(), _ptr(free_start),
+            *[t.data_ptr() for t in outs], n_req, free_pages.numel(), n_tokens, block_table.shape[1], int(page_block),
+            torch.cuda.current_stream(dev).cuda_stream)
+        if rc != 0:
+            raise SmlaError(rc, "sparse_mla_plan_pages")
+        return tuple(outs)
+
+    return _on_stream(stream, dev, call)
+
+
+def sparse_mla_append_kv(c_kv, k_pe, slots, kv_pool, norm_weight=None, eps=1e-6, positions=None, rope=None, q_pe=None,
+                         q=None, stream=None):
+    """Writes the rows of n new tokens into the paged cache: the latent part c_kv [n, 512] bf16
+    (RMS-normalised with norm_weight [512] bf16 and eps when given) and, for d_qk 576, the rotary
+    part k_pe [n, 64] bf16 (turned pair by pair when rope is given), to row slots[t] (int32; a
+    token whose slot lies outside the pool is not written) of kv_pool [rows, 1, d_qk] bf16.  rope
+    [max_pos, 64] fp32 holds 32 cosines and 32 sines per position, positions [n] int32 the tokens'
+    (outside the table: padding, nothing is written).  With q_pe [n, h, 64] bf16, q[..., 512:] of q
+    [n, h, 576] gets the queries' columns turned by the same angles.  c_kv, k_pe and q_pe may be
+    strided views (slices of a projection's output) with a contiguous last dimension.  Returns
+    kv_pool."""
+    lib = load_library()
+    bf16 = torch.bfloat16
+    _check(kv_pool, "kv_pool", bf16)
+    dev = kv_pool.device
+    _check(slots, "slots", torch.int32, dev)
+    _check(positions, "positions", torch.int32, dev)
+    _check(rope, "rope", torch.float32, dev)
+    _check(norm_weight, "norm_weight", bf16, dev)
+    n, d_qk = slots.numel(), kv_pool.shape[-1] if kv_pool.dim() > 1 else 0
+    pool_rows = kv_pool.shape[0]
+    if d_qk not in (512, 576) or kv_pool.numel() != pool_rows * d_qk:
+        raise ValueError("kv_pool must be [rows, 1, d_qk] with d_qk 512 or 576")
+    _check_strided(c_kv, "c_kv", (n, 512), dev)
+    if (k_pe is not None) != (d_qk == 576):
+        raise ValueError("k_pe must be given exactly when d_qk is 576")
+    if k_pe is not None:
+        _check_strided(k_pe, "k_pe", (n, 64), dev)
+    if norm_weight is not None and norm_weight.numel() != 512:
+        raise ValueError("norm_weight must have 512 entries")
+    if rope is not None:
+        if d_qk != 576 or positions is None:
+            raise ValueError("rope needs positions and d_qk 576")
+        if rope.dim() != 2 or rope.shape[1] != 64 or rope.shape[0] < 1:
+            raise ValueError("rope must be [max_pos, 64]")
+        _check_shape(positions, "positions", (n,))
+    if (q_pe is None) != (q is None) or (q_pe is not None and rope is None):
+        raise ValueError("q_pe and q come together, and need rope")
+    h_q = 0
+    if q is not None:
+        _check(q, "q", bf16, dev)
+        if q.dim() != 3 or q.shape[0] != n or q.shape[2] != 576:
+            raise ValueError("q must be [n, h, 576]")
+        h_q = q.shape[1]
+        _check_strided(q_pe, "q_pe", (n, h_q, 64), dev)
+
+    def call():
+        rc = lib.sparse_mla_append_kv(
+            c_kv.data_ptr(), c_kv.stride(0), _ptr(k_pe), 0 if k_pe is None else k_pe.stride(0), slots.data_ptr(),
+            _ptr(positions) if rope is not None else None, _ptr(rope), 0 if rope is None else rope.shape[0],
+            _ptr(norm_weight), float(eps), _ptr(q_pe), 0 if q is None else q_pe.stride(0),
+            0 if q is None else q_pe.stride(1), _ptr(q), h_q, kv_pool.data_ptr(), pool_rows, d_qk, n,
+            torch.cuda.current_stream(dev).cuda_stream)
+        if rc != 0:
+            raise SmlaError(rc, "sparse_mla_append_kv")
+        return kv_pool
+
+    return _on_stream(stream, dev, call) if n else kv_pool
+
+
+def sparse_mla_chunk_fwd_paged(q, kv_pool, block_table, cu_seqlens_q, seqlens_k, page_block=64, causal=True,
+                               attn_sink=None, sm_scale=None, d_v=512, out=None, lse=None, max_logits=None,
+                               workspace=None, stream=None):
+    """Dense attention of each request's new tokens over its paged cache.  q [n_tok, h, d_qk] bf16
+    (any h up to 1024), rows cu_seqlens_q[b] .. cu_seqlens_q[b+1]-1 being request b's new tokens;
+    kv_pool, block_table and page_block as for :func:`sparse_mla_fwd_paged`; seqlens_k [n_req] int32
+    counts the cached keys with the new tokens' own; causal: a token sees the positions up to its
+    own, else every key.  Returns (out [n_tok, h, d_v] bf16, lse [n_tok, h] fp32, max_logits [n_tok,
+    h] fp32); rows of no request are not written.  `workspace` (uint8, at least
+    sparse_mla_chunk_workspace_size bytes, 256-byte aligned) is allocated here when not given; calls
+    that may overlap must not share one."""
+    lib = load_library()
+    _check(q, "q", torch.bfloat16)
+    dev = q.device
+    _check(kv_pool, "kv_pool", torch.bfloat16, dev)
+    _check(block_table, "block_table", torch.int32, dev)
+    _check(cu_seqlens_q, "cu_seqlens_q", torch.int32, dev)
+    _check(seqlens_k, "seqlens_k", torch.int32, dev)
+    _check(attn_sink, "attn_sink", torch.float32, dev)
+    _check(workspace, "workspace", torch.uint8, dev)
+    if q.dim() != 3:
+        raise ValueError("q must be [n_tok, h, d_qk]")
+    n_tok, h_q, d_qk = q.shape
+    pool_rows = kv_pool.shape[0] if kv_pool.dim() else 0
+    if kv_pool.numel() != pool_rows * d_qk:
+        raise ValueError("kv_pool must be [rows, 1, d_qk] with the d_qk of q")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [n_req, max_blocks]")
+    n_req, max_blocks = block_table.shape
+    if seqlens_k.numel() != n_req or cu_seqlens_q.numel() != n_req + 1:
+        raise ValueError("seqlens_k must have n_req entries and cu_seqlens_q n_req + 1")
+    if attn_sink is not None and attn_sink.numel() != h_q:
+        raise ValueError("attn_sink must have h entries")
+    if sm_scale is None:
+        sm_scale = 1.0 / math.sqrt(d_qk) if d_qk else 1.0
+
+    def call():
+        outs = _outputs(q, h_q, d_v, out, lse, max_logits)
+        need = lib.sparse_mla_chunk_workspace_size(n_tok, h_q)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if workspace is None else workspace
+        rc = lib.sparse_mla_chunk_fwd_paged(
+            q.data_ptr(), kv_pool.data_ptr(), pool_rows, block_table.data_ptr(), max_blocks, int(page_block),
+            cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), n_req, 1 if causal else 0, _ptr(attn_sink), float(sm_scale),
+            int(d_v), outs[0].data_ptr(), outs[1].data_ptr(), outs[2].data_ptr(), n_tok, h_q, d_qk, ws.data_ptr(),
+            ws.numel(), torch.cuda.current_stream(dev).cuda_stream)
+        if rc != 0:
+            raise SmlaError(rc, "sparse_mla_chunk_fwd_paged")
+        return outs
+
+    return _on_stream(stream, dev, call)
 
 
 def sparse_mla_device_status(reset=False) -> int:

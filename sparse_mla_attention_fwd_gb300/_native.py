@@ -18,7 +18,8 @@ STATUS_NAMES = {0: "SMLA_OK", 1: "SMLA_ERR_NULL_PTR", 2: "SMLA_ERR_BAD_SHAPE",
 EXPORTED = ("sparse_mla_fwd", "sparse_mla_fwd_paged", "sparse_mla_splitkv_workspace_size",
             "sparse_mla_fwd_splitkv", "sparse_mla_fwd_paged_splitkv", "sparse_mla_fwd_paged_splitkv_static",
             "sparse_mla_fwd_host", "sparse_mla_selftest_wait_timeout", "sparse_mla_device_status",
-            "sparse_mla_status_string", "sparse_mla_abi_version", "sparse_mla_bwd")
+            "sparse_mla_status_string", "sparse_mla_abi_version", "sparse_mla_bwd", "sparse_mla_plan_pages",
+            "sparse_mla_append_kv", "sparse_mla_chunk_workspace_size", "sparse_mla_chunk_fwd_paged")
 
 _lock = threading.Lock()
 _lib = None
@@ -73,6 +74,16 @@ def load_library(path: str | None = None):
         lib.sparse_mla_abi_version.argtypes = []
         lib.sparse_mla_bwd.restype = I32
         lib.sparse_mla_bwd.argtypes = [P, P, P, P, P, P, P, P, F32, I32, P, P, P, I64, I64, I32, I32, I32, P]
+        lib.sparse_mla_plan_pages.restype = I32
+        lib.sparse_mla_plan_pages.argtypes = [P, P, P, P, P, P, P, P, P, P, I64, I64, I64, I32, I32, P]
+        lib.sparse_mla_append_kv.restype = I32
+        lib.sparse_mla_append_kv.argtypes = [P, I64, P, I64, P, P, P, I64, P, F32, P, I64, I64, P, I32, P, I64, I32,
+                                             I64, P]
+        lib.sparse_mla_chunk_workspace_size.restype = SZ
+        lib.sparse_mla_chunk_workspace_size.argtypes = [I64, I32]
+        lib.sparse_mla_chunk_fwd_paged.restype = I32
+        lib.sparse_mla_chunk_fwd_paged.argtypes = [P, P, I64, P, I32, I32, P, P, I64, I32, P, F32, I32, P, P, P, I64,
+                                                   I32, I32, P, SZ, P]
         _lib = lib
         return lib
 

@@ -1,7 +1,7 @@
 """In-tree build of the CUDA library (sm_103a only).
 
-``build()`` compiles ``csrc/sparse_mla_fwd.cu`` with nvcc into ``libsparse_mla_gb300.so`` next
-to this file.  It is what ``__graft_entry__.build()`` runs on every machine (nvcc cross-compiles
+``build()`` compiles the sources of ``csrc/`` with nvcc, one process per file, and links them
+into ``libsparse_mla_gb300.so`` next to this file.  It is what ``__graft_entry__.build()`` runs on every machine (nvcc cross-compiles
 without a GPU); the product path never compiles anything implicitly.
 """
 from __future__ import annotations
@@ -14,7 +14,7 @@ PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
 LIB_NAME = "libsparse_mla_gb300.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
-SOURCES = [os.path.join(PKG_DIR, "csrc", "sparse_mla_fwd.cu")]
+SOURCES = [os.path.join(PKG_DIR, "csrc", f) for f in ("sparse_mla_fwd.cu", "chunk_fwd.cu", "paged_cache.cu")]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -35,12 +35,21 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB_PATH
     nvcc = os.environ.get("NVCC", "nvcc")
     tmp = LIB_PATH + f".tmp{os.getpid()}"
-    cmd = [nvcc, *ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
-           "-o", tmp, *SOURCES]
+    flags = [*ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC"]
     if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, LIB_PATH)
+        flags.insert(0, "-Xptxas=-v")
+    objects = [f"{tmp}.{i}.o" for i in range(len(SOURCES))]
+    try:
+        jobs = [subprocess.Popen([nvcc, *flags, "-c", "-o", o, src]) for o, src in zip(objects, SOURCES)]
+        for src, code in [(src, job.wait()) for src, job in zip(SOURCES, jobs)]:
+            if code != 0:
+                raise RuntimeError(f"nvcc failed on {src} (exit code {code})")
+        subprocess.run([nvcc, *ARCH_FLAGS, "-shared", "-Xcompiler", "-fPIC", "-o", tmp, *objects], check=True)
+        os.replace(tmp, LIB_PATH)
+    finally:
+        for f in [tmp, *objects]:
+            if os.path.exists(f):
+                os.remove(f)
     return LIB_PATH
 
 
