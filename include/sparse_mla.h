@@ -342,6 +342,9 @@ smla_status sparse_mla_chunk_fwd_paged(const void* q, const void* kv_pool, int64
                                        float* max_logits, int64_t n_tok, int h_q, int d_qk, void* workspace,
                                        size_t workspace_bytes, smla_stream_t stream);
 
+/* sparse_mla_device_status of sparse_mla_chunk_fwd_paged's kernel, which has its own word. */
+smla_status sparse_mla_chunk_device_status(int reset);
+
 /* Static, human-readable description of a status code.  Never NULL. */
 const char* sparse_mla_status_string(smla_status status);
 

@@ -568,8 +568,10 @@ def sparse_mla_chunk_fwd_paged(q, kv_pool, block_table, cu_seqlens_q, seqlens_k,
 
 
 def sparse_mla_device_status(reset=False) -> int:
-    """Device-side status word (0, or 5 = a bounded wait gave up); synchronises."""
-    return int(load_library().sparse_mla_device_status(1 if reset else 0))
+    """Device-side status (0, or 5 = a bounded wait of some kernel gave up); synchronises."""
+    lib, reset = load_library(), 1 if reset else 0
+    words = int(lib.sparse_mla_device_status(reset)), int(lib.sparse_mla_chunk_device_status(reset))
+    return words[0] or words[1]
 
 
 def sparse_mla_status_string(code: int) -> str:

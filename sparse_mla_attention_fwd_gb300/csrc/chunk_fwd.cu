@@ -5,25 +5,77 @@
 // the keys at positions j <= that (causal) or every j < L_b.  With K = row[:d_qk], V = row[:512]:
 //   s_j = sm_scale <q, K_j>, m = max s_j, l = sum exp(s_j - m),
 //   O = sum exp(s_j - m) V_j / (l + [sink] exp(sink_h - m)), lse = m + ln l, max_logits = m.
+//
+// All heads of a token, and all tokens of a request, read the same rows, so (token, head) pairs are
+// simply rows of one matrix: a tile is 128 of them (whole tokens of one request, or 128 heads of one
+// token when there are more).  O of a tile is 128 x 512 fp32: all of one SM's tensor memory.  So a
+// PAIR of CTAs (a cluster of two, tcgen05 cta_group::2) holds a tile, 64 rows each, which leaves each
+// SM half its tensor memory for scores and, unlike a 64-row tile on one SM, keeps the tensor unit's
+// full width: every product is M = 128 over the pair.  Per block of 64 keys:
+//   S[128 x 64]   = Q K^T     N = 64: each CTA supplies 32 keys (all d_qk columns)
+//   O[128 x 512] += P V       2 x N = 256: each CTA supplies 256 value columns (all 64 keys)
+// Both products find their operands at the same shared-memory offsets in both CTAs.  CTA r's 32 keys
+// lie there as [D0 | D1 | rope] (columns 0-255, 256-511, 512-575).  For P V it needs, of its own
+// keys, the columns of half r, where they already are, and of the other CTA's keys the same columns:
+// these go into D(1-r), whose contents only S needed ("foreign" half), once S is done.  So a row's bytes
+// are loaded 1.44 times per pair instead of twice, and no operand is held twice.
+//
+// Tensor memory of a CTA (128 lanes; row r of the CTA's 64 in lanes r and r + 64): O in columns
+// 0-255 (value columns 0-255 in lanes 0-63, 256-511 in lanes 64-127), S of block b in columns
+// 256 + 32 (b % 4) (keys 0-31 in lanes 0-63, 32-63 in lanes 64-127).
+//
+// Warps (288 threads): 0 scheduler, 1 K loads, 2 foreign-half and Q loads, 3 S issuer, 4-7 softmax
+// and epilogue (TMEM lane quadrants 0-3), 8 PV issuer; the issuers work in the pair's first CTA.
+// Four buffers of keys: S runs up to three blocks ahead of P V, so the second load of a block and the
+// softmax have one to two blocks' time.
+//
+// Work split.  Tiles times key blocks are laid out on one axis, a tile's cost being its keys plus a
+// constant for its start and end, and the axis is cut into equal ranges, one per pair: a long
+// request is spread over many pairs, short ones share one.  Every CTA finds its own range from the
+// lengths with closed-form sums (no host step, no planning launch).  A tile that lies in one range is
+// finished there; parts of a cut tile go to the workspace (at most two per pair) and a second
+// kernel joins them.  Nothing depends on timing, so results are the same bits from call to call.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <cstring>
+#include <mutex>
 
 #include "../../include/sparse_mla.h"
 #include "host_util.cuh"
+#include "pair_ptx.cuh"
 
 namespace smla {
 namespace {
 
 constexpr int kDv = 512;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRescaleLog2 = 8.0f;      // O is rescaled only when a row's maximum grows by > 2^8
+constexpr uint64_t kWaitLimitNs = 2000000000ull;   // every device wait gives up after 2 s
+
+constexpr int kTileRows = 128;            // rows of a tile, 64 per CTA
+constexpr int kKeys = 64;                 // keys of a block, 32 per CTA
+constexpr int kGens = 4;                  // key buffers, S buffers
+constexpr int kRing = 4;                  // block descriptors ahead
+constexpr int kPairThreads = 288;
+constexpr int kMaxPairs = 80;             // ranges the axis is cut into, at most
+constexpr int kTileCost = 128;            // start and end of a tile, in keys
+constexpr int kMinRange = 128;            // shortest range, in keys (at least kKeys)
+constexpr uint32_t kHalfBytes = 16384;    // 32 keys x 256 columns
+constexpr uint32_t kPBytes = 8192;        // 64 rows x 64 keys
+constexpr uint32_t kTmemCols = 512, kTmemS = 256;
+
+enum : uint32_t { kFirst = 1u, kLast = 2u, kEnd = 4u, kDense = 8u };
+
+__device__ int g_chunk_status = 0;        // SMLA_ERR_DEVICE_TIMEOUT once any wait gave up
 
 struct ChunkParams {
-  const __nv_bfloat16* q;
-  const __nv_bfloat16* pool;
   const int32_t* block_table;
   const int32_t* cu_seqlens_q;
   const int32_t* seqlens_k;
@@ -31,106 +83,676 @@ struct ChunkParams {
   __nv_bfloat16* out;
   float* lse;
   float* max_logits;
+  float* part_o;            // [2 pairs][row_cap][512] unnormalised O of a tile's part
+  float* part_stats;        // [2 pairs][3][128]: offset (log2 units), sum, maximum score
+  int4* joins;              // [pairs]: first row, rows, last pair of the cut tile that starts there
   int64_t pool_rows, n_req, n_tok;
   float sm_scale;
   int h_q, max_blocks, page_block, causal;
+  int box;                  // rows of a tiled load: power of two that divides page_block, or 0
+  int tokens_per_tile, groups;   // 128 / h_q and 1, or 1 and the 128-head groups of a token
+  int row_cap;
 };
 
-// One CTA per (token, eight heads), one warp per head; 32 keys a step, one key per lane for the
-// scores, 16 value columns per lane for the output.
-constexpr int kHeads = 8;
-constexpr int kKeys = 32;
+// ------------------------------------------------------------------------ lengths and the axis
+struct Request {
+  int64_t q0, n_q, n_k, keys;   // first row token, tokens, length, readable keys
+};
+
+__device__ __forceinline__ Request request(const ChunkParams& p, int64_t b) {
+  Request r;
+  const int64_t c0 = __ldg(p.cu_seqlens_q + b), c1 = __ldg(p.cu_seqlens_q + b + 1);
+  r.q0 = min(max(c0, static_cast<int64_t>(0)), p.n_tok);
+  r.n_q = min(max(c1, r.q0), p.n_tok) - r.q0;
+  r.n_k = max(__ldg(p.seqlens_k + b), 0);
+  r.keys = min(r.n_k, static_cast<int64_t>(p.max_blocks) * p.page_block);
+  return r;
+}
+
+__device__ __forceinline__ int64_t token_tiles(const ChunkParams& p, const Request& r) {
+  return (r.n_q + p.tokens_per_tile - 1) / p.tokens_per_tile;
+}
+
+// Axis length of the first k token tiles of a request (one head group).  A tile's own length is at
+// least its keys: with fewer keys than tokens the axis counts the tokens.
+__device__ __forceinline__ int64_t axis_of(const ChunkParams& p, const Request& r, int64_t k) {
+  if (!p.causal) return k * (r.n_k + kTileCost);
+  const int64_t base = max(r.n_k - r.n_q, static_cast<int64_t>(0)), n = token_tiles(p, r), t = p.tokens_per_tile;
+  const int64_t ends = k < n ? t * (k * (k + 1) / 2) : t * (n * (n - 1) / 2) + r.n_q;   // sum of min(n_q, (i + 1) t)
+  return k * (base + kTileCost) + (k > 0 ? ends : 0);
+}
+
+// ------------------------------------------------------------------------ shared memory
+struct __align__(16) BlockDesc {
+  int32_t rows[kKeys];   // pool row of each key, -1 where it does not count
+  uint32_t mask[2];      // validity of keys 0-31 / 32-63
+  uint32_t flags;
+  int32_t key0;          // position of the block's first key
+  int32_t q_row, n_rows; // tile: first (token, head) row, rows
+  int32_t pos0;          // position of the tile's first token
+  int32_t key_end;       // keys of the tile
+  int32_t part;          // workspace slot, or -1: the whole tile is done here
+};
+
+struct Control {
+  BlockDesc ring[kRing];
+  float ex[2][128];      // row maxima of the two key halves
+  float sum[128];
+  uint64_t ring_full[kRing], ring_empty[kRing];
+  uint64_t k_full[kGens], x_full[kGens];      // both CTAs' keys / foreign halves have landed (first CTA)
+  uint64_t s_full[kGens], pv_done[kGens];     // S computed / PV done (both CTAs)
+  uint64_t p_full, o_free, q_full;            // first CTA
+  uint32_t tmem_slot;
+  int abort_flag;
+};
+
+struct RangeScan {       // lies in the P tile until the first P is written
+  int64_t warp_sum[kPairThreads / 32];
+  int64_t total;
+  int64_t req, start;    // request in which this pair's range starts, its position on the axis
+};
 
 template <int D_QK>
-__global__ void __launch_bounds__(32 * kHeads) chunk_fwd_kernel(const ChunkParams p) {
-  constexpr int kPitch = D_QK + 8;
-  extern __shared__ uint8_t smem[];
-  __nv_bfloat16* sk = reinterpret_cast<__nv_bfloat16*>(smem);
-  float* sq = reinterpret_cast<float*>(smem + kKeys * kPitch * 2);
-  __shared__ int64_t s_row[kKeys];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t t = blockIdx.x;
-  const int h = blockIdx.y * kHeads + warp;
-  // the request of this token: the last one that starts at or before it
-  int64_t lo = 0, hi = p.n_req;
-  while (hi - lo > 1) {
-    const int64_t mid = (lo + hi) >> 1;
-    if (p.cu_seqlens_q[mid] <= t) lo = mid;
-    else hi = mid;
-  }
-  const int64_t begin = p.cu_seqlens_q[lo], end = p.cu_seqlens_q[lo + 1];
-  if (t < begin || t >= end) return;   // no request's token: its rows are left as they are
-  const int64_t n_k = max(p.seqlens_k[lo], 0);
-  int64_t seen = p.causal ? n_k - (end - begin) + (t - begin) + 1 : n_k;
-  seen = min(max(seen, static_cast<int64_t>(0)), static_cast<int64_t>(p.max_blocks) * p.page_block);
-  const bool live = h < p.h_q;
-  for (int d = lane; d < D_QK; d += 32)
-    sq[warp * D_QK + d] = live ? __bfloat162float(p.q[(t * p.h_q + h) * D_QK + d]) : 0.f;
-  float m = -INFINITY, l = 0.f, o[16] = {};
-  for (int64_t k0 = 0; k0 < seen; k0 += kKeys) {
-    __syncthreads();
-    if (tid < kKeys) {
-      const int64_t j = k0 + tid;
-      int64_t row = -1;
-      if (j < seen) {
-        const int64_t page = p.block_table[lo * p.max_blocks + j / p.page_block];
-        row = page < 0 ? -1 : page * p.page_block + j % p.page_block;
-        if (row >= p.pool_rows) row = -1;
-      }
-      s_row[tid] = row;
-    }
-    __syncthreads();
-    for (int e = tid; e < kKeys * (D_QK / 8); e += 32 * kHeads) {
-      const int j = e / (D_QK / 8), d = e % (D_QK / 8);
-      const uint4 v = s_row[j] < 0 ? make_uint4(0, 0, 0, 0)
-                                   : reinterpret_cast<const uint4*>(p.pool + s_row[j] * D_QK)[d];
-      *reinterpret_cast<uint4*>(sk + j * kPitch + 8 * d) = v;
-    }
-    __syncthreads();
-    float s = 0.f;
-    for (int d = 0; d < D_QK; ++d) s = fmaf(sq[warp * D_QK + d], __bfloat162float(sk[lane * kPitch + d]), s);
-    s = s_row[lane] < 0 ? -INFINITY : s * p.sm_scale;
-    float top = s;
-    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-    top = fmaxf(top, m);
-    const float base = top == -INFINITY ? 0.f : top;
-    const float keep = exp2f((m - base) * kLog2e);
-    const float e = exp2f((s - base) * kLog2e);
-    float sum = e;
-    for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-    l = l * keep + sum;
-    m = top;
-    for (int i = 0; i < 16; ++i) o[i] *= keep;
-    for (int j = 0; j < kKeys; ++j) {
-      const float w = __shfl_sync(0xffffffffu, e, j);
-      for (int i = 0; i < 8; ++i) {
-        const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(sk + j * kPitch + 64 * i + 2 * lane));
-        o[2 * i] = fmaf(w, v.x, o[2 * i]);
-        o[2 * i + 1] = fmaf(w, v.y, o[2 * i + 1]);
-      }
-    }
-  }
-  if (!live) return;
-  const bool empty = !(l > 0.f);
-  const float den = p.attn_sink ? l + exp2f((p.attn_sink[h] - m) * kLog2e) : l;
-  const float inv = empty ? 0.f : 1.f / den;
-  const int64_t r = t * p.h_q + h;
-  for (int i = 0; i < 8; ++i) {
-    const float a = empty ? 0.f : o[2 * i] * inv, b = empty ? 0.f : o[2 * i + 1] * inv;
-    *reinterpret_cast<__nv_bfloat162*>(p.out + r * kDv + 64 * i + 2 * lane) = __floats2bfloat162_rn(a, b);
-  }
-  if (lane == 0) {
-    p.lse[r] = empty ? INFINITY : m + logf(l);
-    p.max_logits[r] = empty ? -INFINITY : m;
+struct Smem {
+  static constexpr int kChunks = D_QK / 64;
+  static constexpr uint32_t kQBytes = 64 * D_QK * 2;
+  static constexpr uint32_t kGenBytes = 32 * D_QK * 2;
+  static constexpr uint32_t kP = kQBytes + kGens * kGenBytes;
+  static constexpr uint32_t kControl = kP + kPBytes;
+  static constexpr uint32_t kBytes = kControl + sizeof(Control);
+};
+static_assert(Smem<576>::kBytes <= 232448, "a CTA's shared memory");
+
+// ------------------------------------------------------------------------ bounded waits
+__device__ __forceinline__ void give_up(volatile int* abort) {
+  *abort = 1;
+  atomicExch(&g_chunk_status, static_cast<int>(SMLA_ERR_DEVICE_TIMEOUT));
+}
+
+__device__ __forceinline__ void wait_on(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (!mbar_wait_bounded(smem_u32(bar), parity, abort, kWaitLimitNs)) give_up(abort);
+}
+
+// Whether a wait of this CTA has given up, agreed on by the warp.
+__device__ __forceinline__ bool stopped(volatile int* abort) { return __any_sync(0xffffffffu, *abort != 0); }
+
+// The same for a barrier on which the other CTA's threads arrive.
+__device__ __forceinline__ void wait_on_pair(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  const uint32_t b = smem_u32(bar);
+  if (mbar_try_wait_cluster(b, parity)) return;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t spins = 1;; ++spins) {
+    if (mbar_try_wait_cluster(b, parity)) return;
+    if ((spins & 63u) == 0u && (*abort || globaltimer_ns() - t0 > kWaitLimitNs)) return give_up(abort);
   }
 }
 
+__device__ __forceinline__ int64_t pair_scan(int64_t v, int64_t* warp_sum) {   // inclusive, over the CTA
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  if (lane == 31) warp_sum[warp] = v;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) v += warp_sum[w];
+  return v;
+}
+
 template <int D_QK>
-smla_status launch(const ChunkParams& p, cudaStream_t stream) {
-  const int smem = kKeys * (D_QK + 8) * 2 + kHeads * D_QK * 4;
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    chunk_fwd_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap box_map,
+                     const __grid_constant__ CUtensorMap row_map, const ChunkParams p) {
+  using L = Smem<D_QK>;
+  constexpr int kChunks = L::kChunks;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* s_q = smem;
+  uint8_t* s_kv = smem + L::kQBytes;
+  uint8_t* s_p = smem + L::kP;
+  Control& c = *reinterpret_cast<Control*>(smem + L::kControl);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_rank();
+  const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  volatile int* abort = &c.abort_flag;
+
+  if (tid == 0) {
+    c.abort_flag = 0;
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(smem_u32(&c.ring_full[i]), 1);
+      mbar_init(smem_u32(&c.ring_empty[i]), rank == 0 ? 8 : 6);   // two loaders, four softmax warps, two issuers
+    }
+    for (int i = 0; i < kGens; ++i) {
+      mbar_init(smem_u32(&c.k_full[i]), 1);
+      mbar_init(smem_u32(&c.x_full[i]), 1);
+      mbar_init(smem_u32(&c.s_full[i]), 1);
+      mbar_init(smem_u32(&c.pv_done[i]), 1);
+    }
+    mbar_init(smem_u32(&c.p_full), 8);     // the softmax warps of both CTAs
+    mbar_init(smem_u32(&c.o_free), 8);
+    mbar_init(smem_u32(&c.q_full), 1);
+    fence_mbar_init();
+  }
+  if (warp == 3) {
+    tmem_alloc_pair(smem_u32(&c.tmem_slot), kTmemCols);
+    tmem_relinquish_pair();
+  }
+  // this pair's range of the axis
+  RangeScan& scan = *reinterpret_cast<RangeScan*>(s_p);
+  int64_t mine = 0;
+  for (int64_t b = tid; b < p.n_req; b += kPairThreads) {
+    const Request r = request(p, b);
+    mine += p.groups * axis_of(p, r, token_tiles(p, r));
+  }
+  const int64_t upto = pair_scan(mine, scan.warp_sum);
+  if (tid == kPairThreads - 1) scan.total = upto;
+  if (tid == 0) scan.req = -1;
+  __syncthreads();
+  const int64_t total = scan.total;
+  const int64_t range = max((total + pairs - 1) / pairs, static_cast<int64_t>(kMinRange));
+  const int64_t v0 = pair * range, v1 = v0 + range;
+  if (v0 < total) {
+    int64_t run = 0;
+    for (int64_t b0 = 0; b0 < p.n_req && run <= v0; b0 += kPairThreads) {
+      int64_t cost = 0;
+      if (b0 + tid < p.n_req) {
+        const Request r = request(p, b0 + tid);
+        cost = p.groups * axis_of(p, r, token_tiles(p, r));
+      }
+      const int64_t end = run + pair_scan(cost, scan.warp_sum);
+      if (end - cost <= v0 && v0 < end) {
+        scan.req = b0 + tid;
+        scan.start = end - cost;
+      }
+      if (tid == kPairThreads - 1) scan.total = end;
+      __syncthreads();
+      run = scan.total;
+      __syncthreads();
+    }
+  }
+  tc_fence_before();
+  cluster_sync();   // barriers and tensor memory of both CTAs are ready
+  tc_fence_after();
+  const uint32_t tmem = c.tmem_slot;
+  const int64_t first_req = scan.req;
+
+  if (warp >= 4 && warp < 8) {
+    // ============================================================ softmax, rescaling, epilogue
+    const int t = tid - 128;                       // TMEM lane
+    const int row = (t & 63) + 64 * static_cast<int>(rank);
+    const int half = t >> 6;                       // keys and value columns of this lane
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(t & 96) << 16);
+    const uint32_t bar_id = 1 + ((t >> 5) & 1);    // the two warps that share rows
+    const float scale2 = p.sm_scale * kLog2e;
+    const uint32_t p_full = map_to_rank(smem_u32(&c.p_full), 0), o_free = map_to_rank(smem_u32(&c.o_free), 0);
+    uint8_t* p_row = s_p + (t & 63) * 128;
+    const int sw = t & 7;
+    float m = -INFINITY, top = -INFINITY, l = 0.f;   // exponent offset (log2 units), max of q.k, sum
+    int64_t b = 0;
+    int limit = 0;                                   // first key position this row does not see
+    // The two warps that share rows meet at one barrier in every round, the last one included, and leave
+    // together, also when a wait gave up.
+    for (;; ++b) {
+      const BlockDesc& d = c.ring[b % kRing];
+      const int g = static_cast<int>(b % kGens);
+      wait_on(&c.ring_full[b % kRing], (b / kRing) & 1, abort);
+      const uint32_t flags = d.flags;
+      if (flags & kEnd) {
+        named_bar_or(bar_id, 64, *abort != 0);
+        break;
+      }
+      const int n_rows = d.n_rows, part = d.part;
+      const int64_t q_row = d.q_row;
+      const uint32_t key_mask = d.mask[half];
+      const int key0 = d.key0 + 32 * half;
+      if (flags & kFirst) {
+        const int64_t seen = p.causal ? static_cast<int64_t>(d.pos0) + (p.groups == 1 ? row / p.h_q : 0) + 1 : d.key_end;
+        limit = row < n_rows ? static_cast<int>(min(max(seen, static_cast<int64_t>(0)), static_cast<int64_t>(d.key_end))) : 0;
+        m = top = -INFINITY;
+        l = 0.f;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&c.ring_empty[b % kRing]));
+      const int n_seen = limit - key0;
+      const uint32_t mask = n_seen >= 32 ? key_mask : n_seen <= 0 ? 0u : key_mask & ((1u << n_seen) - 1u);
+
+      wait_on(&c.s_full[g], (b / kGens) & 1, abort);
+      __syncwarp();
+      tc_fence_after();
+      uint32_t raw[32];
+      tmem_ld32(lanes + kTmemS + 32 * g, raw);
+      tmem_ld_wait();
+      float s[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) s[i] = __uint_as_float(raw[i]);
+      if (mask != 0xffffffffu) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) s[i] = (mask >> i) & 1u ? s[i] : -INFINITY;
+      }
+      float bm = s[0];
+#pragma unroll
+      for (int i = 1; i < 32; ++i) bm = fmaxf(bm, s[i]);
+      c.ex[b & 1][t] = bm;
+      if (named_bar_or(bar_id, 64, *abort != 0)) break;
+      bm = fmaxf(bm, c.ex[b & 1][t ^ 64]);
+      top = fmaxf(top, bm);
+      float alpha = 1.f;
+      if (bm * scale2 > m + kRescaleLog2) {
+        alpha = fast_exp2(m - bm * scale2);   // 0 when m was -inf
+        m = bm * scale2;
+      }
+      const float neg_m = m == -INFINITY ? 0.f : -m;
+      float sum = 0.f;
+      uint32_t w[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float e0 = fast_exp2(fmaf(s[2 * i], scale2, neg_m));
+        const float e1 = fast_exp2(fmaf(s[2 * i + 1], scale2, neg_m));
+        sum += e0 + e1;
+        w[i] = pack_bf16x2(e0, e1);   // the weights of V, as the tensor unit takes them
+      }
+      l = fmaf(l, alpha, sum);
+      // PV of the block before has read the P tile and is done with O
+      if (b > 0) wait_on(&c.pv_done[(b - 1) % kGens], ((b - 1) / kGens) & 1, abort);
+      if (!(flags & kFirst) && __any_sync(0xffffffffu, alpha != 1.f)) {
+        tc_fence_after();
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+          uint32_t o[32];
+          tmem_ld32(lanes + 32 * i, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+          tmem_st32(lanes + 32 * i, o);
+        }
+        tmem_st_wait();
+      }
+      // P tile: 64 rows of 64 keys, 128-byte swizzle
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4*>(p_row + (((4 * half + i) ^ sw) << 4)) =
+            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(p_full);
+
+      if (flags & kLast) {
+        c.sum[t] = l;
+        named_bar_sync(bar_id, 64);
+        l += c.sum[t ^ 64];
+        const bool empty = !(l > 0.f);
+        const bool live = row < n_rows;
+        float inv = 1.f;
+        if (part < 0) {
+          const int64_t r = q_row + row;
+          float den = l;
+          if (p.attn_sink && live) den += exp2f(fmaf(__ldg(p.attn_sink + r % p.h_q), kLog2e, -m));
+          inv = empty ? 0.f : 1.f / den;
+          if (live && half == 0) {
+            p.lse[r] = empty ? INFINITY : (m + log2f(l)) * kLn2;
+            p.max_logits[r] = empty ? -INFINITY : top * p.sm_scale;
+          }
+        } else if (live && half == 0) {
+          float* st = p.part_stats + part * 3 * 128 + row;
+          st[0] = empty ? -INFINITY : m;
+          st[128] = empty ? 0.f : l;
+          st[256] = empty ? -INFINITY : top * p.sm_scale;
+        }
+        wait_on(&c.pv_done[g], (b / kGens) & 1, abort);
+        __syncwarp();
+        tc_fence_after();
+        __nv_bfloat16* out = p.out + (q_row + row) * kDv + 256 * half;
+        float* po = part < 0 ? nullptr : p.part_o + (static_cast<int64_t>(part) * p.row_cap + row) * kDv + 256 * half;
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+          uint32_t o[32];
+          tmem_ld32(lanes + 32 * i, o);
+          tmem_ld_wait();
+          if (live && part < 0) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t v[4];
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const float a = __uint_as_float(o[8 * j + 2 * x]), e = __uint_as_float(o[8 * j + 2 * x + 1]);
+                v[x] = empty ? 0u : pack_bf16x2(a * inv, e * inv);
+              }
+              *reinterpret_cast<uint4*>(out + 32 * i + 8 * j) = make_uint4(v[0], v[1], v[2], v[3]);
+            }
+          } else if (live) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              *reinterpret_cast<uint4*>(po + 32 * i + 4 * j) = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+          }
+          __syncwarp();
+        }
+        // O has been read: the next tile's first PV may overwrite it
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(o_free);
+      }
+    }
+  } else if (warp == 0) {
+    // ============================================================ scheduler
+    int64_t b = 0;
+    bool stop = false;
+    auto acquire = [&] {
+      if (b >= kRing) wait_on(&c.ring_empty[b % kRing], ((b / kRing) - 1) & 1, abort);
+      stop = stopped(abort);
+    };
+    auto publish = [&] {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&c.ring_full[b % kRing]));
+      ++b;
+    };
+    int4 join = make_int4(0, 0, -1, 0);
+    bool more = v0 < total && first_req >= 0;
+    int64_t start = more ? scan.start : 0;       // the request's position on the axis
+    for (int64_t req = first_req; more && req < p.n_req && !stop; ++req) {
+      const Request r = request(p, req);
+      const int64_t n_tiles = token_tiles(p, r);
+      const int64_t before = r.n_k - r.n_q;      // position of the request's first new token
+      int64_t k = 0;
+      if (start < v0) {   // the range starts inside this request: last token tile that begins at or before v0
+        int64_t lo = 0, hi = n_tiles;
+        while (hi - lo > 1) {
+          const int64_t mid = (lo + hi) >> 1;
+          if (p.groups * axis_of(p, r, mid) <= v0 - start) lo = mid;
+          else hi = mid;
+        }
+        k = lo;
+      }
+      for (; k < n_tiles && more && !stop; ++k) {
+        const int64_t at = axis_of(p, r, k), size = axis_of(p, r, k + 1) - at;
+        const int64_t tok = k * p.tokens_per_tile, last = min(r.n_q, tok + p.tokens_per_tile);
+        const int64_t key_end = p.causal ? min(max(before + last, static_cast<int64_t>(0)), r.keys) : r.keys;
+        const int64_t n_blocks = max((key_end + kKeys - 1) / kKeys, static_cast<int64_t>(1));
+        for (int grp = 0; grp < p.groups && more && !stop; ++grp) {
+          const int64_t s = start + p.groups * at + grp * size;   // the tile's position on the axis
+          if (s >= v1) {
+            more = false;
+            break;
+          }
+          const int64_t j0 = s >= v0 ? 0 : (v0 - s + kKeys - 1) / kKeys;
+          const int64_t j1 = min(n_blocks, (v1 - s + kKeys - 1) / kKeys);
+          if (j0 >= j1) continue;
+          const int64_t q_row = (r.q0 + tok) * p.h_q + (p.groups > 1 ? kTileRows * grp : 0);
+          const int n_rows = p.groups > 1 ? min(kTileRows, p.h_q - kTileRows * grp) : static_cast<int>(last - tok) * p.h_q;
+          int part = -1;
+          if (j0 > 0) part = static_cast<int>(2 * pair);
+          else if (j1 < n_blocks) {
+            part = static_cast<int>(2 * pair + 1);
+            join = make_int4(static_cast<int>(q_row), n_rows, static_cast<int>((s + kKeys * (n_blocks - 1)) / range), 0);
+          }
+          for (int64_t j = j0; j < j1 && !stop; ++j) {
+            int32_t pool_row[2];
+            uint32_t mask[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const int64_t pos = kKeys * j + 32 * x + lane;
+              int64_t at_row = -1;
+              if (pos < key_end) {   // so the column is below max_blocks
+                const int col = static_cast<int>(pos) / p.page_block;
+                const int64_t page = __ldg(p.block_table + req * p.max_blocks + col);
+                at_row = page * p.page_block + (static_cast<int>(pos) - col * p.page_block);
+                if (page < 0 || at_row >= p.pool_rows) at_row = -1;
+              }
+              pool_row[x] = static_cast<int32_t>(at_row);
+              mask[x] = __ballot_sync(0xffffffffu, at_row >= 0);
+            }
+            acquire();
+            BlockDesc& d = c.ring[b % kRing];
+            d.rows[lane] = pool_row[0];
+            d.rows[32 + lane] = pool_row[1];
+            if (lane == 0) {
+              d.mask[0] = mask[0];
+              d.mask[1] = mask[1];
+              d.flags = (j == j0 ? kFirst : 0u) | (j == j1 - 1 ? kLast : 0u) |
+                        (p.box > 0 && (mask[0] & mask[1]) == 0xffffffffu ? kDense : 0u);
+              d.key0 = static_cast<int32_t>(kKeys * j);
+              d.q_row = static_cast<int32_t>(q_row);
+              d.n_rows = n_rows;
+              d.pos0 = static_cast<int32_t>(before + tok);
+              d.key_end = static_cast<int32_t>(key_end);
+              d.part = part;
+            }
+            publish();
+          }
+        }
+      }
+      start += p.groups * axis_of(p, r, n_tiles);
+    }
+    acquire();
+    if (lane == 0) {
+      c.ring[b % kRing].flags = kEnd;
+      if (rank == 0) p.joins[pair] = join;
+    }
+    publish();
+  } else if (warp == 1 || warp == 2) {
+    // ============================================================ loads
+    // Warp 1: all columns of the CTA's own 32 keys.  Warp 2: Q at a tile's start, and the CTA's value
+    // columns of the other CTA's 32 keys.  Blocks whose 64 keys all count go by tiled loads of
+    // `box` rows (within a page); any other by row gathers, where a key that does not count has row
+    // -1 and reads as zeros.
+    const bool foreign = warp == 2;
+    const uint32_t k_full = map_to_rank(smem_u32(&c.k_full[0]), 0), x_full = map_to_rank(smem_u32(&c.x_full[0]), 0);
+    const uint32_t q_full = map_to_rank(smem_u32(&c.q_full), 0);
+    const int keys0 = 32 * static_cast<int>(foreign ? 1 - rank : rank);   // the keys of the block that this warp loads
+    const int chunk0 = foreign ? 4 * static_cast<int>(rank) : 0;          // first 64-column chunk, chunks, first place
+    const int n_chunks = foreign ? 4 : kChunks;
+    const uint32_t dst0 = foreign ? (1 - rank) * kHalfBytes : 0;
+    const uint32_t bytes = n_chunks * 4096u;
+    for (int64_t b = 0;; ++b) {
+      const BlockDesc& d = c.ring[b % kRing];
+      const int g = static_cast<int>(b % kGens);
+      wait_on(&c.ring_full[b % kRing], (b / kRing) & 1, abort);
+      if (stopped(abort)) break;
+      const uint32_t flags = d.flags;
+      if (flags & kEnd) break;
+      if (foreign) {
+        if (flags & kFirst) {   // this warp has seen S of every earlier block done: Q is free
+          if (rank == 0 && lane == 0) mbar_arrive_expect_tx(smem_u32(&c.q_full), 2 * L::kQBytes);
+          if (lane < kChunks)
+            tma_load_2d_pair(smem_u32(s_q + lane * 8192), &q_map, 64 * lane, d.q_row + 64 * static_cast<int>(rank), q_full);
+        }
+        wait_on(&c.s_full[g], (b / kGens) & 1, abort);   // S has read the foreign half
+      } else if (b >= kGens) {
+        wait_on(&c.pv_done[g], ((b / kGens) - 1) & 1, abort);
+      }
+      if (stopped(abort)) break;
+      const uint32_t bar = (foreign ? x_full : k_full) + 8 * g;
+      if (rank == 0 && lane == 0) mbar_arrive_expect_tx(smem_u32(foreign ? &c.x_full[g] : &c.k_full[g]), 2 * bytes);
+      const uint32_t dst = smem_u32(s_kv) + g * L::kGenBytes + dst0;
+      if (flags & kDense) {
+        const int n = n_chunks * (32 / p.box);
+        for (int i = lane; i < n; i += 32) {
+          const int grp = i / n_chunks, ch = i - grp * n_chunks, k0 = grp * p.box;
+          tma_load_2d_pair(dst + ch * 4096 + k0 * 128, &box_map, 64 * (chunk0 + ch), d.rows[keys0 + k0], bar);
+        }
+      } else {
+        for (int i = lane; i < 8 * n_chunks; i += 32) {
+          const int ch = i >> 3, k0 = 4 * (i & 7);
+          const int4 rr = *reinterpret_cast<const int4*>(&d.rows[keys0 + k0]);
+          tma_gather4_pair(dst + ch * 4096 + k0 * 128, &row_map, 64 * (chunk0 + ch), rr.x, rr.y, rr.z, rr.w, bar);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&c.ring_empty[b % kRing]));
+    }
+  } else if (warp == 3 && rank == 0) {
+    // ============================================================ S issuer
+    if (lane == 0) {
+      constexpr uint32_t idesc = make_idesc_bf16(kTileRows, kKeys, false, false);
+      const uint64_t qd = make_sdesc_sw128(smem_u32(s_q), 16, 1024);
+      int64_t tiles = 0;
+      for (int64_t b = 0; !*abort; ++b) {
+        const int g = static_cast<int>(b % kGens);
+        wait_on(&c.ring_full[b % kRing], (b / kRing) & 1, abort);
+        const uint32_t flags = c.ring[b % kRing].flags;
+        mbar_arrive(smem_u32(&c.ring_empty[b % kRing]));
+        if (flags & kEnd) break;
+        if (flags & kFirst) wait_on(&c.q_full, tiles++ & 1, abort);
+        // the keys have landed; their loads waited for PV of block b - 4, so S buffer g has been read
+        wait_on(&c.k_full[g], (b / kGens) & 1, abort);
+        tc_fence_after();
+        const uint64_t kd = make_sdesc_sw128(smem_u32(s_kv) + g * L::kGenBytes, 16, 1024);
+#pragma unroll
+        for (int ks = 0; ks < D_QK / 16; ++ks)
+          umma_ss_pair(tmem + kTmemS + 32 * g, qd + (((ks >> 2) * 8192 + (ks & 3) * 32) >> 4),
+                       kd + (((ks >> 2) * 4096 + (ks & 3) * 32) >> 4), idesc, ks > 0 ? 1u : 0u);
+        umma_commit_pair(smem_u32(&c.s_full[g]));
+      }
+    }
+    __syncwarp();
+  } else if (warp == 8 && rank == 0) {
+    // ============================================================ PV issuer
+    if (lane == 0) {
+      constexpr uint32_t idesc = make_idesc_bf16(kTileRows, 256, false, true);
+      const uint64_t pd = make_sdesc_sw128(smem_u32(s_p), 16, 1024);
+      int64_t tiles = 0;
+      for (int64_t b = 0; !*abort; ++b) {
+        const int g = static_cast<int>(b % kGens);
+        wait_on(&c.ring_full[b % kRing], (b / kRing) & 1, abort);
+        const uint32_t flags = c.ring[b % kRing].flags;
+        mbar_arrive(smem_u32(&c.ring_empty[b % kRing]));
+        if (flags & kEnd) break;
+        const bool first = (flags & kFirst) != 0;
+        if (first) {   // the tile before has been read out of O
+          if (tiles > 0) wait_on_pair(&c.o_free, (tiles - 1) & 1, abort);
+          ++tiles;
+        }
+        wait_on(&c.x_full[g], (b / kGens) & 1, abort);
+        wait_on_pair(&c.p_full, b & 1, abort);
+        tc_fence_after();
+        // keys 0-31 in D0, 32-63 in D1, in both CTAs (own and foreign, or foreign and own)
+        const uint64_t vd = make_sdesc_sw128(smem_u32(s_kv) + g * L::kGenBytes, 4096, 1024);
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int ks = 0; ks < kKeys / 16; ++ks)
+            umma_ss_pair(tmem + 128 * n, pd + ((ks * 32) >> 4),
+                         vd + (((ks >> 1) * kHalfBytes + n * 8192 + (ks & 1) * 2048) >> 4), idesc,
+                         (!first || ks > 0) ? 1u : 0u);
+        umma_commit_pair(smem_u32(&c.pv_done[g]));
+      }
+    }
+    __syncwarp();
+  }
+
+  // ---- every copy and product has been waited for (each tile's epilogue follows its last PV) unless a
+  // wait gave up; then what is still in flight gets time to land before the CTAs leave
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  if (*abort) {
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 5000000ull) {
+    }
+  }
+  cluster_sync();
+  if (warp == 3) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, kTmemCols);
+  }
+}
+
+// ------------------------------------------------------------------------ joining cut tiles
+// A tile cut over pairs w .. w1 left its parts in slots 2w + 1, 2(w+1), .., 2 w1.  With M = max m_i:
+//   l = sum 2^(m_i - M) l_i,   O = sum 2^(m_i - M) O_i / (l + [sink] 2^(sink log2 e - M)).
+constexpr int kJoinRows = 4;
+constexpr int kJoinThreads = 128 * kJoinRows;   // four value columns a thread
+
+__global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const ChunkParams p) {
+  const int w = blockIdx.x;
+  const int4 join = p.joins[w];
+  const int row = blockIdx.y * kJoinRows + (threadIdx.x >> 7), t = threadIdx.x & 127;
+  if (join.z < 0 || row >= join.y) return;
+  auto slot = [&](int i) { return i == w ? 2 * w + 1 : 2 * i; };
+  float M = -INFINITY, top = -INFINITY;
+  for (int i = w; i <= join.z; ++i) {
+    const float* st = p.part_stats + slot(i) * 3 * 128 + row;
+    M = fmaxf(M, st[0]);
+    top = fmaxf(top, st[256]);
+  }
+  float l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (M > -INFINITY) {
+#pragma unroll 4
+    for (int i = w; i <= join.z; ++i) {
+      const float* st = p.part_stats + slot(i) * 3 * 128 + row;
+      const float4 o = reinterpret_cast<const float4*>(p.part_o + (static_cast<int64_t>(slot(i)) * p.row_cap + row) * kDv)[t];
+      const float a = exp2f(st[0] - M);
+      l = fmaf(a, st[128], l);
+      acc.x = fmaf(a, o.x, acc.x);
+      acc.y = fmaf(a, o.y, acc.y);
+      acc.z = fmaf(a, o.z, acc.z);
+      acc.w = fmaf(a, o.w, acc.w);
+    }
+  }
+  const bool empty = !(l > 0.f);
+  const int64_t r = static_cast<int64_t>(join.x) + row;
+  float den = l;
+  if (p.attn_sink && !empty) den += exp2f(fmaf(__ldg(p.attn_sink + r % p.h_q), kLog2e, -M));
+  const float inv = empty ? 0.f : 1.f / den;
+  uint2 v = make_uint2(0u, 0u);
+  if (!empty) v = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  reinterpret_cast<uint2*>(p.out + r * kDv)[t] = v;
+  if (t == 0) {
+    p.lse[r] = empty ? INFINITY : (M + log2f(l)) * kLn2;
+    p.max_logits[r] = empty ? -INFINITY : top;
+  }
+}
+
+// ------------------------------------------------------------------------ host side
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  return fn;
+}
+
+// Boxes of 64 columns x box_rows of a row-major bf16 matrix, 128-byte swizzle.
+bool make_map(CUtensorMap* m, const void* base, int64_t rows, int cols, int box_rows) {
+  const auto fn = encode_fn();
+  if (!fn) return false;
+  std::memset(m, 0, sizeof(*m));
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
+  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)}, es[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Workspace {
+  size_t stats, joins, bytes;   // offsets behind part_o
+};
+Workspace workspace_of(int64_t n_tok, int h_q) {
+  const int64_t cap = n_tok * h_q < kTileRows ? n_tok * h_q : kTileRows;
+  Workspace w;
+  w.stats = static_cast<size_t>(2 * kMaxPairs) * cap * kDv * 4;   // multiples of 256
+  w.joins = w.stats + 2 * kMaxPairs * 3 * 128 * 4;
+  w.bytes = w.joins + ((kMaxPairs * sizeof(int4) + 255) & ~static_cast<size_t>(255));
+  return w;
+}
+
+template <int D_QK>
+smla_status launch(const CUtensorMap& qm, const CUtensorMap& bm, const CUtensorMap& rm, const ChunkParams& p, int pairs,
+                   cudaStream_t stream) {
+  constexpr int smem = Smem<D_QK>::kBytes;
   if (cudaFuncSetAttribute(chunk_fwd_kernel<D_QK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return SMLA_ERR_LAUNCH;
-  chunk_fwd_kernel<D_QK><<<dim3(static_cast<unsigned>(p.n_tok), (p.h_q + kHeads - 1) / kHeads), 32 * kHeads, smem, stream>>>(p);
+  chunk_fwd_kernel<D_QK><<<2 * pairs, kPairThreads, smem, stream>>>(qm, bm, rm, p);
+  if (cudaGetLastError() != cudaSuccess) return SMLA_ERR_LAUNCH;
+  chunk_join_kernel<<<dim3(pairs, kTileRows / kJoinRows), kJoinThreads, 0, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? SMLA_OK : SMLA_ERR_LAUNCH;
 }
 
@@ -142,9 +764,8 @@ using namespace smla;
 extern "C" {
 
 size_t sparse_mla_chunk_workspace_size(int64_t n_tok, int h_q) {
-  (void)n_tok;
-  (void)h_q;
-  return 0;
+  if (n_tok <= 0 || h_q < 1 || h_q > 1024 || n_tok > INT32_MAX / h_q) return 0;
+  return workspace_of(n_tok, h_q).bytes;
 }
 
 smla_status sparse_mla_chunk_fwd_paged(const void* q, const void* kv_pool, int64_t pool_rows,
@@ -166,11 +787,14 @@ smla_status sparse_mla_chunk_fwd_paged(const void* q, const void* kv_pool, int64
       !aligned_to(max_logits, 4) || !aligned_to(block_table, 4) || !aligned_to(cu_seqlens_q, 4) ||
       !aligned_to(seqlens_k, 4) || !aligned_to(attn_sink, 4))
     return SMLA_ERR_MISALIGNED;
-  if (workspace_bytes < sparse_mla_chunk_workspace_size(n_tok, h_q)) return SMLA_ERR_WORKSPACE;
-  (void)workspace;
+  const Workspace ws = workspace_of(n_tok, h_q);
+  if (!workspace || workspace_bytes < ws.bytes) return SMLA_ERR_WORKSPACE;
+  if (!aligned_to(workspace, 256)) return SMLA_ERR_MISALIGNED;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 2)
+    return SMLA_ERR_LAUNCH;
   ChunkParams p{};
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.pool = static_cast<const __nv_bfloat16*>(kv_pool);
   p.block_table = block_table;
   p.cu_seqlens_q = cu_seqlens_q;
   p.seqlens_k = seqlens_k;
@@ -178,6 +802,9 @@ smla_status sparse_mla_chunk_fwd_paged(const void* q, const void* kv_pool, int64
   p.out = static_cast<__nv_bfloat16*>(out);
   p.lse = lse;
   p.max_logits = max_logits;
+  p.part_o = static_cast<float*>(workspace);
+  p.part_stats = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + ws.stats);
+  p.joins = reinterpret_cast<int4*>(static_cast<uint8_t*>(workspace) + ws.joins);
   p.pool_rows = pool_rows;
   p.n_req = n_req;
   p.n_tok = n_tok;
@@ -186,8 +813,28 @@ smla_status sparse_mla_chunk_fwd_paged(const void* q, const void* kv_pool, int64
   p.max_blocks = max_blocks;
   p.page_block = page_block;
   p.causal = causal != 0;
+  // boxes of 8 rows and more keep the 128-byte swizzle's 8-row pattern; smaller pages go by gathers
+  p.box = page_block % 32 == 0 ? 32 : page_block % 16 == 0 ? 16 : page_block % 8 == 0 ? 8 : 0;
+  p.tokens_per_tile = h_q <= kTileRows ? kTileRows / h_q : 1;
+  p.groups = h_q <= kTileRows ? 1 : (h_q + kTileRows - 1) / kTileRows;
+  p.row_cap = static_cast<int>(n_tok * h_q < kTileRows ? n_tok * h_q : kTileRows);
+  CUtensorMap qm, bm, rm;
+  if (!make_map(&qm, q, n_tok * h_q, d_qk, 64) || !make_map(&bm, kv_pool, pool_rows, d_qk, p.box ? p.box : 8) ||
+      !make_map(&rm, kv_pool, pool_rows, d_qk, 1))
+    return SMLA_ERR_TENSOR_MAP;
+  const int pairs = sms / 2 < kMaxPairs ? sms / 2 : kMaxPairs;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return d_qk == 512 ? launch<512>(p, s) : launch<576>(p, s);
+  return d_qk == 512 ? launch<512>(qm, bm, rm, p, pairs, s) : launch<576>(qm, bm, rm, p, pairs, s);
+}
+
+smla_status sparse_mla_chunk_device_status(int reset) {
+  int v = 0;
+  if (cudaMemcpyFromSymbol(&v, g_chunk_status, sizeof(int)) != cudaSuccess) return SMLA_ERR_LAUNCH;
+  if (reset) {
+    const int z = 0;
+    if (cudaMemcpyToSymbol(g_chunk_status, &z, sizeof(int)) != cudaSuccess) return SMLA_ERR_LAUNCH;
+  }
+  return static_cast<smla_status>(v);
 }
 
 }  // extern "C"
