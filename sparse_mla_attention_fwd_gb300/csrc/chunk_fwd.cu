@@ -212,7 +212,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   uint8_t* s_p = smem + L::kP;
   Control& c = *reinterpret_cast<Control*>(smem + L::kControl);
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const uint32_t rank = cluster_rank();
   const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   volatile int* abort = &c.abort_flag;
@@ -376,7 +376,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(p_full);
+      if (lane == 0) mbar_arrive_pair(p_full);
 
       if (flags & kLast) {
         c.sum[t] = l;
@@ -431,7 +431,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         // O has been read: the next tile's first PV may overwrite it
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(o_free);
+        if (lane == 0) mbar_arrive_pair(o_free);
       }
     }
   } else if (warp == 0) {
@@ -583,7 +583,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
   } else if (warp == 3 && rank == 0) {
     // ============================================================ S issuer
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t idesc = make_idesc_bf16(kTileRows, kKeys, false, false);
       const uint64_t qd = make_sdesc_sw128(smem_u32(s_q), 16, 1024);
       int64_t tiles = 0;
@@ -608,7 +608,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     __syncwarp();
   } else if (warp == 8 && rank == 0) {
     // ============================================================ PV issuer
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t idesc = make_idesc_bf16(kTileRows, 256, false, true);
       const uint64_t pd = make_sdesc_sw128(smem_u32(s_p), 16, 1024);
       int64_t tiles = 0;

@@ -14,6 +14,19 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 
+// True in one lane of a converged warp, always the same one.  The compiler knows that a branch on it
+// has one active thread and keeps the operands of the instructions there in uniform registers: a thread that
+// issues tcgen05.mma in such a branch needs under 25 cycles for each, under a lane == 0 branch 44 to 53.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred P;\n\t"
+      "elect.sync _|P, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, P;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
 // Every thread of both CTAs.
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -26,8 +39,12 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
   return r;
 }
 
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+// Arrival on a barrier of either CTA of the pair, releasing at CTA scope.  That is enough for what the pair's
+// threads publish to each other here: operands in their own CTA's shared or tensor memory, which only their
+// own SM's tensor core reads (behind fence.proxy.async and tcgen05.fence).  A release at cluster scope
+// drains the SM's memory traffic first: 1700 to 2900 cycles for each arrival under load.
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
