@@ -202,8 +202,9 @@ __device__ __forceinline__ int64_t pair_scan(int64_t v, int64_t* warp_sum) {   /
 
 template <int D_QK>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
-    chunk_fwd_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap box_map,
-                     const __grid_constant__ CUtensorMap row_map, const ChunkParams p) {
+    chunk_fwd_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap half_map,
+                     const __grid_constant__ CUtensorMap box_map, const __grid_constant__ CUtensorMap row_map,
+                     const ChunkParams p) {
   using L = Smem<D_QK>;
   constexpr int kChunks = L::kChunks;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -289,15 +290,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     uint8_t* p_row = s_p + (t & 63) * 128;
     const int sw = t & 7;
     float m = -INFINITY, top = -INFINITY, l = 0.f;   // exponent offset (log2 units), max of q.k, sum
-    int64_t b = 0;
+    int b = 0;
     int limit = 0;                                   // first key position this row does not see
     // The two warps that share rows meet at one barrier in every round, the last one included, and leave
     // together, also when a wait gave up.
     for (;; ++b) {
       const BlockDesc& d = c.ring[b % kRing];
-      const int g = static_cast<int>(b % kGens);
+      const int g = b % kGens;
       wait_on(&c.ring_full[b % kRing], (b / kRing) & 1, abort);
-      const uint32_t flags = d.flags;
+      __syncwarp();
+      const uint32_t flags = __shfl_sync(0xffffffffu, d.flags, 0);
       if (flags & kEnd) {
         named_bar_or(bar_id, 64, *abort != 0);
         break;
@@ -436,7 +438,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
   } else if (warp == 0) {
     // ============================================================ scheduler
-    int64_t b = 0;
+    int b = 0;
     bool stop = false;
     auto acquire = [&] {
       if (b >= kRing) wait_on(&c.ring_empty[b % kRing], ((b / kRing) - 1) & 1, abort);
@@ -533,52 +535,68 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   } else if (warp == 1 || warp == 2) {
     // ============================================================ loads
     // Warp 1: all columns of the CTA's own 32 keys.  Warp 2: Q at a tile's start, and the CTA's value
-    // columns of the other CTA's 32 keys.  Blocks whose 64 keys all count go by tiled loads of
-    // `box` rows (within a page); any other by row gathers, where a key that does not count has row
-    // -1 and reads as zeros.
+    // columns of the other CTA's 32 keys.  Blocks whose 64 keys all count go by tiled loads: 32 rows
+    // of four 64-column chunks at once where pages allow it, else boxes of 8 or 16 rows of a chunk.
+    // One elected thread issues them: issued from several lanes, each load costs the warp a turn.  Any
+    // other block goes by row gathers, where a key that does not count has row -1 and reads as zeros.
     const bool foreign = warp == 2;
     const uint32_t k_full = map_to_rank(smem_u32(&c.k_full[0]), 0), x_full = map_to_rank(smem_u32(&c.x_full[0]), 0);
     const uint32_t q_full = map_to_rank(smem_u32(&c.q_full), 0);
     const int keys0 = 32 * static_cast<int>(foreign ? 1 - rank : rank);   // the keys of the block that this warp loads
-    const int chunk0 = foreign ? 4 * static_cast<int>(rank) : 0;          // first 64-column chunk, chunks, first place
-    const int n_chunks = foreign ? 4 : kChunks;
-    const uint32_t dst0 = foreign ? (1 - rank) * kHalfBytes : 0;
-    const uint32_t bytes = n_chunks * 4096u;
-    for (int64_t b = 0;; ++b) {
+    // four 64-column chunks from chunk0 on go to dst, the rope chunk to `rope` (if not 0)
+    auto load = [&](const BlockDesc& d, bool dense, int chunk0, uint32_t dst, uint32_t rope, uint32_t bar) {
+      if (dense) {
+        if (elect_one()) {
+          if (p.box == 32) {
+            const int row = d.rows[keys0];
+            tma_load_3d_pair(dst, &half_map, 0, row, chunk0, bar);
+            if (rope) tma_load_2d_pair(rope, &box_map, 512, row, bar);
+          } else {
+            for (int k0 = 0; k0 < 32; k0 += p.box) {
+              const int row = d.rows[keys0 + k0];
+              for (int ch = 0; ch < 4; ++ch)
+                tma_load_2d_pair(dst + ch * 4096 + k0 * 128, &box_map, 64 * (chunk0 + ch), row, bar);
+              if (rope) tma_load_2d_pair(rope + k0 * 128, &box_map, 512, row, bar);
+            }
+          }
+        }
+      } else {
+        const int k0 = 4 * (lane & 7), ch = lane >> 3;   // eight groups of four rows, four chunks
+        const int4 rr = *reinterpret_cast<const int4*>(&d.rows[keys0 + k0]);
+        tma_gather4_pair(dst + ch * 4096 + k0 * 128, &row_map, 64 * (chunk0 + ch), rr.x, rr.y, rr.z, rr.w, bar);
+        if (rope && lane < 8) tma_gather4_pair(rope + k0 * 128, &row_map, 512, rr.x, rr.y, rr.z, rr.w, bar);
+      }
+      __syncwarp();
+    };
+    for (int b = 0;; ++b) {
       const BlockDesc& d = c.ring[b % kRing];
-      const int g = static_cast<int>(b % kGens);
+      const int g = b % kGens;
       wait_on(&c.ring_full[b % kRing], (b / kRing) & 1, abort);
       if (stopped(abort)) break;
       const uint32_t flags = d.flags;
       if (flags & kEnd) break;
+      const bool dense = (flags & kDense) != 0;
+      const uint32_t gen = smem_u32(s_kv) + g * L::kGenBytes;
       if (foreign) {
         if (flags & kFirst) {   // this warp has seen S of every earlier block done: Q is free
-          if (rank == 0 && lane == 0) mbar_arrive_expect_tx(smem_u32(&c.q_full), 2 * L::kQBytes);
-          if (lane < kChunks)
-            tma_load_2d_pair(smem_u32(s_q + lane * 8192), &q_map, 64 * lane, d.q_row + 64 * static_cast<int>(rank), q_full);
+          if (elect_one()) {
+            if (rank == 0) mbar_arrive_expect_tx(smem_u32(&c.q_full), 2 * L::kQBytes);
+            const int row = d.q_row + 64 * static_cast<int>(rank);
+            for (int ch = 0; ch < kChunks; ++ch) tma_load_2d_pair(smem_u32(s_q + ch * 8192), &q_map, 64 * ch, row, q_full);
+          }
+          __syncwarp();
         }
         wait_on(&c.s_full[g], (b / kGens) & 1, abort);   // S has read the foreign half
-      } else if (b >= kGens) {
-        wait_on(&c.pv_done[g], ((b / kGens) - 1) & 1, abort);
-      }
-      if (stopped(abort)) break;
-      const uint32_t bar = (foreign ? x_full : k_full) + 8 * g;
-      if (rank == 0 && lane == 0) mbar_arrive_expect_tx(smem_u32(foreign ? &c.x_full[g] : &c.k_full[g]), 2 * bytes);
-      const uint32_t dst = smem_u32(s_kv) + g * L::kGenBytes + dst0;
-      if (flags & kDense) {
-        const int n = n_chunks * (32 / p.box);
-        for (int i = lane; i < n; i += 32) {
-          const int grp = i / n_chunks, ch = i - grp * n_chunks, k0 = grp * p.box;
-          tma_load_2d_pair(dst + ch * 4096 + k0 * 128, &box_map, 64 * (chunk0 + ch), d.rows[keys0 + k0], bar);
-        }
+        if (stopped(abort)) break;
+        if (rank == 0 && lane == 0) mbar_arrive_expect_tx(smem_u32(&c.x_full[g]), 2 * kHalfBytes);
+        load(d, dense, 4 * static_cast<int>(rank), gen + (1 - rank) * kHalfBytes, 0u, x_full + 8 * g);
       } else {
-        for (int i = lane; i < 8 * n_chunks; i += 32) {
-          const int ch = i >> 3, k0 = 4 * (i & 7);
-          const int4 rr = *reinterpret_cast<const int4*>(&d.rows[keys0 + k0]);
-          tma_gather4_pair(dst + ch * 4096 + k0 * 128, &row_map, 64 * (chunk0 + ch), rr.x, rr.y, rr.z, rr.w, bar);
-        }
+        if (b >= kGens) wait_on(&c.pv_done[g], ((b / kGens) - 1) & 1, abort);
+        if (stopped(abort)) break;
+        if (rank == 0 && lane == 0) mbar_arrive_expect_tx(smem_u32(&c.k_full[g]), 2 * L::kGenBytes);
+        load(d, dense, 0, gen, kChunks > 8 ? gen + 2 * kHalfBytes : 0u, k_full + 8 * g);
+        load(d, dense, 4, gen + kHalfBytes, 0u, k_full + 8 * g);
       }
-      __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&c.ring_empty[b % kRing]));
     }
   } else if (warp == 3 && rank == 0) {
@@ -587,8 +605,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       constexpr uint32_t idesc = make_idesc_bf16(kTileRows, kKeys, false, false);
       const uint64_t qd = make_sdesc_sw128(smem_u32(s_q), 16, 1024);
       int64_t tiles = 0;
-      for (int64_t b = 0; !*abort; ++b) {
-        const int g = static_cast<int>(b % kGens);
+      for (int b = 0; !*abort; ++b) {
+        const int g = b % kGens;
         wait_on(&c.ring_full[b % kRing], (b / kRing) & 1, abort);
         const uint32_t flags = c.ring[b % kRing].flags;
         mbar_arrive(smem_u32(&c.ring_empty[b % kRing]));
@@ -612,8 +630,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       constexpr uint32_t idesc = make_idesc_bf16(kTileRows, 256, false, true);
       const uint64_t pd = make_sdesc_sw128(smem_u32(s_p), 16, 1024);
       int64_t tiles = 0;
-      for (int64_t b = 0; !*abort; ++b) {
-        const int g = static_cast<int>(b % kGens);
+      for (int b = 0; !*abort; ++b) {
+        const int g = b % kGens;
         wait_on(&c.ring_full[b % kRing], (b / kRing) & 1, abort);
         const uint32_t flags = c.ring[b % kRing].flags;
         mbar_arrive(smem_u32(&c.ring_empty[b % kRing]));
@@ -651,6 +669,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     while (globaltimer_ns() - t0 < 5000000ull) {
     }
   }
+  __syncwarp();
   cluster_sync();
   if (warp == 3) {
     tc_fence_after();
@@ -719,15 +738,19 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// Boxes of 64 columns x box_rows of a row-major bf16 matrix, 128-byte swizzle.
-bool make_map(CUtensorMap* m, const void* base, int64_t rows, int cols, int box_rows) {
+// Boxes of box_rows rows x box_chunks chunks of 64 columns of a row-major bf16 matrix, chunk after chunk, 128-byte
+// swizzle.  One chunk: a 2-D map, addressed by column and row; more: 3-D, by 0, row and chunk.
+bool make_map(CUtensorMap* m, const void* base, int64_t rows, int cols, int box_rows, int box_chunks = 1) {
   const auto fn = encode_fn();
   if (!fn) return false;
   std::memset(m, 0, sizeof(*m));
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
-  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)}, es[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+  const cuuint64_t pitch = static_cast<cuuint64_t>(cols) * 2;
+  const bool flat = box_chunks == 1;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(flat ? cols : 64), static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(cols / 64)};
+  const cuuint64_t strides[2] = {pitch, 128};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(box_chunks)}, es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, flat ? 2 : 3, const_cast<void*>(base), dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -745,12 +768,12 @@ Workspace workspace_of(int64_t n_tok, int h_q) {
 }
 
 template <int D_QK>
-smla_status launch(const CUtensorMap& qm, const CUtensorMap& bm, const CUtensorMap& rm, const ChunkParams& p, int pairs,
-                   cudaStream_t stream) {
+smla_status launch(const CUtensorMap& qm, const CUtensorMap& hm, const CUtensorMap& bm, const CUtensorMap& rm,
+                   const ChunkParams& p, int pairs, cudaStream_t stream) {
   constexpr int smem = Smem<D_QK>::kBytes;
   if (cudaFuncSetAttribute(chunk_fwd_kernel<D_QK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return SMLA_ERR_LAUNCH;
-  chunk_fwd_kernel<D_QK><<<2 * pairs, kPairThreads, smem, stream>>>(qm, bm, rm, p);
+  chunk_fwd_kernel<D_QK><<<2 * pairs, kPairThreads, smem, stream>>>(qm, hm, bm, rm, p);
   if (cudaGetLastError() != cudaSuccess) return SMLA_ERR_LAUNCH;
   chunk_join_kernel<<<dim3(pairs, kTileRows / kJoinRows), kJoinThreads, 0, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? SMLA_OK : SMLA_ERR_LAUNCH;
@@ -818,13 +841,13 @@ smla_status sparse_mla_chunk_fwd_paged(const void* q, const void* kv_pool, int64
   p.tokens_per_tile = h_q <= kTileRows ? kTileRows / h_q : 1;
   p.groups = h_q <= kTileRows ? 1 : (h_q + kTileRows - 1) / kTileRows;
   p.row_cap = static_cast<int>(n_tok * h_q < kTileRows ? n_tok * h_q : kTileRows);
-  CUtensorMap qm, bm, rm;
-  if (!make_map(&qm, q, n_tok * h_q, d_qk, 64) || !make_map(&bm, kv_pool, pool_rows, d_qk, p.box ? p.box : 8) ||
-      !make_map(&rm, kv_pool, pool_rows, d_qk, 1))
+  CUtensorMap qm, hm, bm, rm;
+  if (!make_map(&qm, q, n_tok * h_q, d_qk, 64) || !make_map(&hm, kv_pool, pool_rows, d_qk, 32, 4) ||
+      !make_map(&bm, kv_pool, pool_rows, d_qk, p.box ? p.box : 8) || !make_map(&rm, kv_pool, pool_rows, d_qk, 1))
     return SMLA_ERR_TENSOR_MAP;
   const int pairs = sms / 2 < kMaxPairs ? sms / 2 : kMaxPairs;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return d_qk == 512 ? launch<512>(qm, bm, rm, p, pairs, s) : launch<576>(qm, bm, rm, p, pairs, s);
+  return d_qk == 512 ? launch<512>(qm, hm, bm, rm, p, pairs, s) : launch<576>(qm, hm, bm, rm, p, pairs, s);
 }
 
 smla_status sparse_mla_chunk_device_status(int reset) {
