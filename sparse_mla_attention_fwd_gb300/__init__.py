@@ -53,6 +53,11 @@ def _stream_handle(stream, device):
     return stream.cuda_stream
 
 
+# the current stream's handle on a device; a stream object in between costs two microseconds
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _check(t, name, dtype, device=None):
     if t is None:
         return
@@ -377,36 +382,45 @@ def sparse_mla_bwd(q, kv, out, dout, indices, lse, topk_length=None, attn_sink=N
     return dq, dkv, dsink
 
 
-def _on_stream(stream, dev, call):
-    """Runs `call` with `stream` as the current one, so that what it allocates belongs to the stream
-    that uses it, and with `dev` as the current device."""
+def _dense(t, name, dtype, dev):
+    """_check for a required tensor on a known CUDA device, with one test in the usual case."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == dev and t.is_contiguous()):
+        _check(t, name, dtype, dev)
+        raise TypeError(f"{name} must be a torch.Tensor")
+
+
+def _strided(t, name, shape, dev):
+    """The strides of a bf16 tensor of this shape whose last dimension is contiguous."""
+    if isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.device == dev and t.shape == shape:
+        strides = t.stride()
+        if strides[-1] == 1 or t.numel() == 0:
+            return strides
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be a torch.bfloat16 tensor")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _first(t, name, dtype):
+    """Checks the tensor whose device the others have to share; returns that device."""
+    _check(t, name, dtype)
+    if t is None:
+        raise TypeError(f"{name} must be a torch.Tensor")
+    return t.device
+
+
+def _on_device(fn, dev, stream, *args, **kwargs):
+    """Calls fn again with `stream` as the current one, so that what it allocates belongs to the stream
+    that uses it, or with the tensors' device as the current one."""
     if stream is not None:
         if stream.device != dev:
             raise ValueError(f"stream is on {stream.device}, the tensors are on {dev}")
         with torch.cuda.stream(stream):
-            return call()
-    if torch.cuda.current_device() == dev.index:
-        return call()
+            return fn(*args, **kwargs)
     with torch.cuda.device(dev):
-        return call()
-
-
-def _check_shape(t, name, shape):
-    if t is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-
-
-def _check_strided(t, name, shape, dev):
-    """A bf16 tensor of this shape whose last dimension is contiguous."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    _check_shape(t, name, shape)
-    if t.numel() and t.stride(-1) != 1:
-        raise ValueError(f"{name} must be contiguous in its last dimension")
+        return fn(*args, **kwargs)
 
 
 def sparse_mla_plan_pages(seqlens, new_lens, block_table, free_pages, n_tokens, page_block=64, free_start=None,
@@ -421,38 +435,46 @@ def sparse_mla_plan_pages(seqlens, new_lens, block_table, free_pages, n_tokens, 
     pages that were missing.  See the C header for the exact rules."""
     lib = load_library()
     i32 = torch.int32
-    _check(seqlens, "seqlens", i32)
-    dev = seqlens.device
-    _check(new_lens, "new_lens", i32, dev)
-    _check(block_table, "block_table", i32, dev)
-    _check(free_pages, "free_pages", i32, dev)
-    _check(free_start, "free_start", i32, dev)
+    dev = _first(seqlens, "seqlens", i32)
+    if stream is not None or torch.cuda.current_device() != dev.index:
+        return _on_device(sparse_mla_plan_pages, dev, stream, seqlens, new_lens, block_table, free_pages, n_tokens, page_block,
+                          free_start, seqlens_k, cu_seqlens_q, slots, positions, counts)
+    _dense(new_lens, "new_lens", i32, dev)
+    _dense(block_table, "block_table", i32, dev)
+    _dense(free_pages, "free_pages", i32, dev)
     n_req, n_tokens = seqlens.numel(), int(n_tokens)
     if n_tokens < 0:
         raise ValueError("n_tokens must be at least 0")
     if new_lens.numel() != n_req:
         raise ValueError("new_lens must have one entry per request")
-    if block_table.dim() != 2 or block_table.shape[0] != n_req:
+    table_shape = block_table.shape
+    if len(table_shape) != 2 or table_shape[0] != n_req:
         raise ValueError("block_table must be [n_req, max_blocks]")
-    if free_start is not None and free_start.numel() != 1:
-        raise ValueError("free_start must have one entry")
-    given = (("seqlens_k", seqlens_k, n_req), ("cu_seqlens_q", cu_seqlens_q, n_req + 1), ("slots", slots, n_tokens),
-             ("positions", positions, n_tokens), ("counts", counts, 3))
-    for name, t, n in given:
-        _check(t, name, i32, dev)
-        _check_shape(t, name, (n,))
-
-    def call():
-        outs = [torch.empty(n, dtype=i32, device=dev) if t is None else t for _, t, n in given]
-        rc = lib.sparse_mla_plan_pages(
-            seqlens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(), _ptr(free_start),
-            *[t.data_ptr() for t in outs], n_req, free_pages.numel(), n_tokens, block_table.shape[1], int(page_block),
-            torch.cuda.current_stream(dev).cuda_stream)
-        if rc != 0:
-            raise SmlaError(rc, "sparse_mla_plan_pages")
-        return tuple(outs)
-
-    return _on_stream(stream, dev, call)
+    if free_start is not None:
+        _dense(free_start, "free_start", i32, dev)
+        if free_start.numel() != 1:
+            raise ValueError("free_start must have one entry")
+    outs, sizes = (seqlens_k, cu_seqlens_q, slots, positions, counts), (n_req, n_req + 1, n_tokens, n_tokens, 3)
+    missing = [n for t, n in zip(outs, sizes) if t is None]
+    if missing:   # one allocation for all of them
+        fresh = iter(torch.empty(sum(missing), dtype=i32, device=dev).split_with_sizes(missing))
+    if len(missing) == 5:
+        outs = tuple(fresh)
+    else:
+        for name, t, n in zip(("seqlens_k", "cu_seqlens_q", "slots", "positions", "counts"), outs, sizes):
+            if t is not None:
+                _dense(t, name, i32, dev)
+                if t.shape != (n,):
+                    raise ValueError(f"{name} must be [{n}], got {list(t.shape)}")
+        outs = tuple(next(fresh) if t is None else t for t in outs)
+    k, cu, sl, pos, cnt = outs
+    rc = lib.sparse_mla_plan_pages(
+        seqlens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(), _ptr(free_start),
+        k.data_ptr(), cu.data_ptr(), sl.data_ptr(), pos.data_ptr(), cnt.data_ptr(), n_req, free_pages.numel(), n_tokens,
+        table_shape[1], int(page_block), _raw_stream(dev.index))
+    if rc != 0:
+        raise SmlaError(rc, "sparse_mla_plan_pages")
+    return outs
 
 
 def sparse_mla_append_kv(c_kv, k_pe, slots, kv_pool, norm_weight=None, eps=1e-6, positions=None, rope=None, q_pe=None,
@@ -468,51 +490,54 @@ def sparse_mla_append_kv(c_kv, k_pe, slots, kv_pool, norm_weight=None, eps=1e-6,
     kv_pool."""
     lib = load_library()
     bf16 = torch.bfloat16
-    _check(kv_pool, "kv_pool", bf16)
-    dev = kv_pool.device
-    _check(slots, "slots", torch.int32, dev)
-    _check(positions, "positions", torch.int32, dev)
-    _check(rope, "rope", torch.float32, dev)
-    _check(norm_weight, "norm_weight", bf16, dev)
-    n, d_qk = slots.numel(), kv_pool.shape[-1] if kv_pool.dim() > 1 else 0
-    pool_rows = kv_pool.shape[0]
+    dev = _first(kv_pool, "kv_pool", bf16)
+    if stream is not None or torch.cuda.current_device() != dev.index:
+        return _on_device(sparse_mla_append_kv, dev, stream, c_kv, k_pe, slots, kv_pool, norm_weight, eps, positions, rope, q_pe, q)
+    _dense(slots, "slots", torch.int32, dev)
+    pool_shape = kv_pool.shape
+    n, d_qk, pool_rows = slots.numel(), pool_shape[-1] if len(pool_shape) > 1 else 0, pool_shape[0]
     if d_qk not in (512, 576) or kv_pool.numel() != pool_rows * d_qk:
         raise ValueError("kv_pool must be [rows, 1, d_qk] with d_qk 512 or 576")
-    _check_strided(c_kv, "c_kv", (n, 512), dev)
+    c_stride, k_stride, q_strides, h_q, max_pos = _strided(c_kv, "c_kv", (n, 512), dev)[0], 0, (0, 0), 0, 0
     if (k_pe is not None) != (d_qk == 576):
         raise ValueError("k_pe must be given exactly when d_qk is 576")
     if k_pe is not None:
-        _check_strided(k_pe, "k_pe", (n, 64), dev)
-    if norm_weight is not None and norm_weight.numel() != 512:
-        raise ValueError("norm_weight must have 512 entries")
+        k_stride = _strided(k_pe, "k_pe", (n, 64), dev)[0]
+    if norm_weight is not None:
+        _dense(norm_weight, "norm_weight", bf16, dev)
+        if norm_weight.numel() != 512:
+            raise ValueError("norm_weight must have 512 entries")
     if rope is not None:
         if d_qk != 576 or positions is None:
             raise ValueError("rope needs positions and d_qk 576")
-        if rope.dim() != 2 or rope.shape[1] != 64 or rope.shape[0] < 1:
+        _dense(rope, "rope", torch.float32, dev)
+        _dense(positions, "positions", torch.int32, dev)
+        rope_shape = rope.shape
+        if len(rope_shape) != 2 or rope_shape[1] != 64 or rope_shape[0] < 1:
             raise ValueError("rope must be [max_pos, 64]")
-        _check_shape(positions, "positions", (n,))
+        max_pos = rope_shape[0]
+        if positions.numel() != n:
+            raise ValueError("positions must have one entry per token")
+    else:
+        positions = None
     if (q_pe is None) != (q is None) or (q_pe is not None and rope is None):
         raise ValueError("q_pe and q come together, and need rope")
-    h_q = 0
     if q is not None:
-        _check(q, "q", bf16, dev)
-        if q.dim() != 3 or q.shape[0] != n or q.shape[2] != 576:
+        _dense(q, "q", bf16, dev)
+        q_shape = q.shape
+        if len(q_shape) != 3 or q_shape[0] != n or q_shape[2] != 576:
             raise ValueError("q must be [n, h, 576]")
-        h_q = q.shape[1]
-        _check_strided(q_pe, "q_pe", (n, h_q, 64), dev)
-
-    def call():
-        rc = lib.sparse_mla_append_kv(
-            c_kv.data_ptr(), c_kv.stride(0), _ptr(k_pe), 0 if k_pe is None else k_pe.stride(0), slots.data_ptr(),
-            _ptr(positions) if rope is not None else None, _ptr(rope), 0 if rope is None else rope.shape[0],
-            _ptr(norm_weight), float(eps), _ptr(q_pe), 0 if q is None else q_pe.stride(0),
-            0 if q is None else q_pe.stride(1), _ptr(q), h_q, kv_pool.data_ptr(), pool_rows, d_qk, n,
-            torch.cuda.current_stream(dev).cuda_stream)
-        if rc != 0:
-            raise SmlaError(rc, "sparse_mla_append_kv")
+        h_q = q_shape[1]
+        q_strides = _strided(q_pe, "q_pe", (n, h_q, 64), dev)
+    if n == 0:
         return kv_pool
-
-    return _on_stream(stream, dev, call) if n else kv_pool
+    rc = lib.sparse_mla_append_kv(
+        c_kv.data_ptr(), c_stride, _ptr(k_pe), k_stride, slots.data_ptr(), _ptr(positions), _ptr(rope), max_pos,
+        _ptr(norm_weight), float(eps), _ptr(q_pe), q_strides[0], q_strides[1], _ptr(q), h_q, kv_pool.data_ptr(), pool_rows,
+        d_qk, n, _raw_stream(dev.index))
+    if rc != 0:
+        raise SmlaError(rc, "sparse_mla_append_kv")
+    return kv_pool
 
 
 def sparse_mla_chunk_fwd_paged(q, kv_pool, block_table, cu_seqlens_q, seqlens_k, page_block=64, causal=True,
@@ -527,44 +552,53 @@ def sparse_mla_chunk_fwd_paged(q, kv_pool, block_table, cu_seqlens_q, seqlens_k,
     sparse_mla_chunk_workspace_size bytes, 256-byte aligned) is allocated here when not given; calls
     that may overlap must not share one."""
     lib = load_library()
-    _check(q, "q", torch.bfloat16)
-    dev = q.device
-    _check(kv_pool, "kv_pool", torch.bfloat16, dev)
-    _check(block_table, "block_table", torch.int32, dev)
-    _check(cu_seqlens_q, "cu_seqlens_q", torch.int32, dev)
-    _check(seqlens_k, "seqlens_k", torch.int32, dev)
-    _check(attn_sink, "attn_sink", torch.float32, dev)
-    _check(workspace, "workspace", torch.uint8, dev)
-    if q.dim() != 3:
+    bf16, i32, f32 = torch.bfloat16, torch.int32, torch.float32
+    dev = _first(q, "q", bf16)
+    if stream is not None or torch.cuda.current_device() != dev.index:
+        return _on_device(sparse_mla_chunk_fwd_paged, dev, stream, q, kv_pool, block_table, cu_seqlens_q, seqlens_k, page_block,
+                          causal, attn_sink, sm_scale, d_v, out, lse, max_logits, workspace)
+    _dense(kv_pool, "kv_pool", bf16, dev)
+    _dense(block_table, "block_table", i32, dev)
+    _dense(cu_seqlens_q, "cu_seqlens_q", i32, dev)
+    _dense(seqlens_k, "seqlens_k", i32, dev)
+    q_shape, pool_shape, table_shape = q.shape, kv_pool.shape, block_table.shape
+    if len(q_shape) != 3:
         raise ValueError("q must be [n_tok, h, d_qk]")
-    n_tok, h_q, d_qk = q.shape
-    pool_rows = kv_pool.shape[0] if kv_pool.dim() else 0
+    n_tok, h_q, d_qk = q_shape
+    pool_rows = pool_shape[0] if len(pool_shape) else 0
     if kv_pool.numel() != pool_rows * d_qk:
         raise ValueError("kv_pool must be [rows, 1, d_qk] with the d_qk of q")
-    if block_table.dim() != 2:
+    if len(table_shape) != 2:
         raise ValueError("block_table must be [n_req, max_blocks]")
-    n_req, max_blocks = block_table.shape
+    n_req, max_blocks = table_shape
     if seqlens_k.numel() != n_req or cu_seqlens_q.numel() != n_req + 1:
         raise ValueError("seqlens_k must have n_req entries and cu_seqlens_q n_req + 1")
-    if attn_sink is not None and attn_sink.numel() != h_q:
-        raise ValueError("attn_sink must have h entries")
+    if attn_sink is not None:
+        _dense(attn_sink, "attn_sink", f32, dev)
+        if attn_sink.numel() != h_q:
+            raise ValueError("attn_sink must have h entries")
     if sm_scale is None:
         sm_scale = 1.0 / math.sqrt(d_qk) if d_qk else 1.0
-
-    def call():
-        outs = _outputs(q, h_q, d_v, out, lse, max_logits)
-        need = lib.sparse_mla_chunk_workspace_size(n_tok, h_q)
-        ws = torch.empty(need, dtype=torch.uint8, device=dev) if workspace is None else workspace
-        rc = lib.sparse_mla_chunk_fwd_paged(
-            q.data_ptr(), kv_pool.data_ptr(), pool_rows, block_table.data_ptr(), max_blocks, int(page_block),
-            cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), n_req, 1 if causal else 0, _ptr(attn_sink), float(sm_scale),
-            int(d_v), outs[0].data_ptr(), outs[1].data_ptr(), outs[2].data_ptr(), n_tok, h_q, d_qk, ws.data_ptr(),
-            ws.numel(), torch.cuda.current_stream(dev).cuda_stream)
-        if rc != 0:
-            raise SmlaError(rc, "sparse_mla_chunk_fwd_paged")
-        return outs
-
-    return _on_stream(stream, dev, call)
+    if out is None and lse is None and max_logits is None:
+        out = torch.empty((n_tok, h_q, d_v), dtype=bf16, device=dev)
+        lse = torch.empty((n_tok, h_q), dtype=f32, device=dev)
+        max_logits = torch.empty((n_tok, h_q), dtype=f32, device=dev)
+    else:
+        out, lse, max_logits = _outputs(q, h_q, d_v, out, lse, max_logits)
+    if workspace is None:
+        ws_bytes = lib.sparse_mla_chunk_workspace_size(n_tok, h_q)
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    else:
+        _dense(workspace, "workspace", torch.uint8, dev)
+        ws_bytes = workspace.numel()
+    rc = lib.sparse_mla_chunk_fwd_paged(
+        q.data_ptr(), kv_pool.data_ptr(), pool_rows, block_table.data_ptr(), max_blocks, int(page_block),
+        cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), n_req, 1 if causal else 0, _ptr(attn_sink), float(sm_scale), int(d_v),
+        out.data_ptr(), lse.data_ptr(), max_logits.data_ptr(), n_tok, h_q, d_qk, workspace.data_ptr(), ws_bytes,
+        _raw_stream(dev.index))
+    if rc != 0:
+        raise SmlaError(rc, "sparse_mla_chunk_fwd_paged")
+    return out, lse, max_logits
 
 
 def sparse_mla_device_status(reset=False) -> int:

@@ -40,6 +40,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -110,7 +111,7 @@ __device__ __forceinline__ Request request(const ChunkParams& p, int64_t b) {
 }
 
 __device__ __forceinline__ int64_t token_tiles(const ChunkParams& p, const Request& r) {
-  return (r.n_q + p.tokens_per_tile - 1) / p.tokens_per_tile;
+  return (static_cast<uint32_t>(r.n_q) + p.tokens_per_tile - 1u) / static_cast<uint32_t>(p.tokens_per_tile);
 }
 
 // Axis length of the first k token tiles of a request (one head group).  A tile's own length is at
@@ -213,6 +214,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   uint8_t* s_p = smem + L::kP;
   Control& c = *reinterpret_cast<Control*>(smem + L::kControl);
 
+  cudaTriggerProgrammaticLaunchCompletion();   // the joining kernel may come up; it waits for this one's end
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const uint32_t rank = cluster_rank();
   const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -239,21 +241,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     tmem_alloc_pair(smem_u32(&c.tmem_slot), kTmemCols);
     tmem_relinquish_pair();
   }
-  // this pair's range of the axis
+  if (tid == 32) {
+    prefetch_map(&q_map);
+    prefetch_map(&half_map);
+    prefetch_map(&box_map);
+    prefetch_map(&row_map);
+  }
+  tc_fence_before();
+  __syncwarp();
+  cluster_arrive();   // barriers and tensor memory of this CTA are ready
+  // This pair's range of the axis: the requests' lengths summed, then the request found in which the
+  // range starts (from the same sums when each thread has one request at most).
   RangeScan& scan = *reinterpret_cast<RangeScan*>(s_p);
   int64_t mine = 0;
   for (int64_t b = tid; b < p.n_req; b += kPairThreads) {
     const Request r = request(p, b);
     mine += p.groups * axis_of(p, r, token_tiles(p, r));
   }
+  if (tid == 0) scan.req = -1;
   const int64_t upto = pair_scan(mine, scan.warp_sum);
   if (tid == kPairThreads - 1) scan.total = upto;
-  if (tid == 0) scan.req = -1;
   __syncthreads();
   const int64_t total = scan.total;
   const int64_t range = max((total + pairs - 1) / pairs, static_cast<int64_t>(kMinRange));
   const int64_t v0 = pair * range, v1 = v0 + range;
-  if (v0 < total) {
+  if (p.n_req <= kPairThreads) {
+    if (upto - mine <= v0 && v0 < upto) {
+      scan.req = tid;
+      scan.start = upto - mine;
+    }
+    __syncthreads();
+  } else if (v0 < total) {
     int64_t run = 0;
     for (int64_t b0 = 0; b0 < p.n_req && run <= v0; b0 += kPairThreads) {
       int64_t cost = 0;
@@ -272,8 +290,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       __syncthreads();
     }
   }
-  tc_fence_before();
-  cluster_sync();   // barriers and tensor memory of both CTAs are ready
+  __syncwarp();
+  cluster_wait();     // and those of the other CTA
   tc_fence_after();
   const uint32_t tmem = c.tmem_slot;
   const int64_t first_req = scan.req;
@@ -405,14 +423,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         wait_on(&c.pv_done[g], (b / kGens) & 1, abort);
         __syncwarp();
         tc_fence_after();
-        __nv_bfloat16* out = p.out + (q_row + row) * kDv + 256 * half;
-        float* po = part < 0 ? nullptr : p.part_o + (static_cast<int64_t>(part) * p.row_cap + row) * kDv + 256 * half;
+        // A lane holds a row's 256 values; stored as they are, each store instruction would touch 32
+        // rows.  They go through the warp's quarter of the P tile (PV has read it), 64 bytes of 32
+        // rows at a time, and leave with four lanes a row.
+        const int warp_row = row - lane;   // the warp's first row of the tile
+        uint8_t* stage = s_p + (t >> 5) * 2048;
+        uint8_t* put = stage + lane * 64;
+        const int put_sw = (lane >> 1) & 3, get_row = lane >> 2;
+        const uint8_t* get = stage + get_row * 64 + (((lane & 3) ^ ((get_row >> 1) & 3)) << 4);
+        const bool whole = part < 0;
+        // where this lane's 16 bytes of rows get_row, get_row + 8, .. go
+        uint8_t* dst = whole ? reinterpret_cast<uint8_t*>(p.out + (q_row + warp_row + get_row) * kDv + 256 * half)
+                             : reinterpret_cast<uint8_t*>(
+                                   p.part_o + (static_cast<int64_t>(part) * p.row_cap + warp_row + get_row) * kDv + 256 * half);
+        dst += 16 * (lane & 3);
+        const int64_t row_bytes = whole ? kDv * 2 : kDv * 4;
+        const int rows_left = n_rows - warp_row - get_row;
+        auto flush = [&] {
+          __syncwarp();
+#pragma unroll
+          for (int x = 0; x < 4; ++x)   // rows 8 x + get_row; the swizzle repeats every eight rows
+            if (8 * x < rows_left)
+              *reinterpret_cast<uint4*>(dst + 8 * x * row_bytes) = *reinterpret_cast<const uint4*>(get + 512 * x);
+          __syncwarp();
+          dst += 64;
+        };
 #pragma unroll 1
         for (int i = 0; i < 8; ++i) {
           uint32_t o[32];
           tmem_ld32(lanes + 32 * i, o);
           tmem_ld_wait();
-          if (live && part < 0) {
+          if (whole) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               uint32_t v[4];
@@ -421,14 +462,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 const float a = __uint_as_float(o[8 * j + 2 * x]), e = __uint_as_float(o[8 * j + 2 * x + 1]);
                 v[x] = empty ? 0u : pack_bf16x2(a * inv, e * inv);
               }
-              *reinterpret_cast<uint4*>(out + 32 * i + 8 * j) = make_uint4(v[0], v[1], v[2], v[3]);
+              *reinterpret_cast<uint4*>(put + ((j ^ put_sw) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
             }
-          } else if (live) {
+            flush();
+          } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              *reinterpret_cast<uint4*>(po + 32 * i + 4 * j) = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            for (int y = 0; y < 2; ++y) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<uint4*>(put + ((j ^ put_sw) << 4)) =
+                    make_uint4(o[16 * y + 4 * j], o[16 * y + 4 * j + 1], o[16 * y + 4 * j + 2], o[16 * y + 4 * j + 3]);
+              flush();
+            }
           }
-          __syncwarp();
         }
         // O has been read: the next tile's first PV may overwrite it
         tc_fence_before();
@@ -685,6 +731,7 @@ constexpr int kJoinThreads = 128 * kJoinRows;   // four value columns a thread
 
 __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const ChunkParams p) {
   const int w = blockIdx.x;
+  cudaGridDependencySynchronize();
   const int4 join = p.joins[w];
   const int row = blockIdx.y * kJoinRows + (threadIdx.x >> 7), t = threadIdx.x & 127;
   if (join.z < 0 || row >= join.y) return;
@@ -767,16 +814,38 @@ Workspace workspace_of(int64_t n_tok, int h_q) {
   return w;
 }
 
+// SMs of the current device; 0 on an error.  Asked once per device, with the kernels' shared-memory limit set
+// there at the same time.
+int device_sms() {
+  constexpr int kDevices = 64;
+  static std::atomic<int> sms[kDevices];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 0;
+  if ((n = sms[dev].load(std::memory_order_acquire)) > 0) return n;
+  if (cudaFuncSetAttribute(chunk_fwd_kernel<512>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<512>::kBytes) != cudaSuccess ||
+      cudaFuncSetAttribute(chunk_fwd_kernel<576>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<576>::kBytes) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  sms[dev].store(n, std::memory_order_release);
+  return n;
+}
+
 template <int D_QK>
 smla_status launch(const CUtensorMap& qm, const CUtensorMap& hm, const CUtensorMap& bm, const CUtensorMap& rm,
                    const ChunkParams& p, int pairs, cudaStream_t stream) {
-  constexpr int smem = Smem<D_QK>::kBytes;
-  if (cudaFuncSetAttribute(chunk_fwd_kernel<D_QK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return SMLA_ERR_LAUNCH;
-  chunk_fwd_kernel<D_QK><<<2 * pairs, kPairThreads, smem, stream>>>(qm, hm, bm, rm, p);
+  chunk_fwd_kernel<D_QK><<<2 * pairs, kPairThreads, Smem<D_QK>::kBytes, stream>>>(qm, hm, bm, rm, p);
   if (cudaGetLastError() != cudaSuccess) return SMLA_ERR_LAUNCH;
-  chunk_join_kernel<<<dim3(pairs, kTileRows / kJoinRows), kJoinThreads, 0, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? SMLA_OK : SMLA_ERR_LAUNCH;
+  // the joining kernel's CTAs come up while the first one still runs, and wait for its end
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(pairs, (p.row_cap + kJoinRows - 1) / kJoinRows);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = stream;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, chunk_join_kernel, p) == cudaSuccess ? SMLA_OK : SMLA_ERR_LAUNCH;
 }
 
 }  // namespace
@@ -813,10 +882,8 @@ smla_status sparse_mla_chunk_fwd_paged(const void* q, const void* kv_pool, int64
   const Workspace ws = workspace_of(n_tok, h_q);
   if (!workspace || workspace_bytes < ws.bytes) return SMLA_ERR_WORKSPACE;
   if (!aligned_to(workspace, 256)) return SMLA_ERR_MISALIGNED;
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 2)
-    return SMLA_ERR_LAUNCH;
+  const int sms = device_sms();
+  if (sms < 2) return SMLA_ERR_LAUNCH;
   ChunkParams p{};
   p.block_table = block_table;
   p.cu_seqlens_q = cu_seqlens_q;
