@@ -454,19 +454,16 @@ def sparse_mla_plan_pages(seqlens, new_lens, block_table, free_pages, n_tokens, 
         _dense(free_start, "free_start", i32, dev)
         if free_start.numel() != 1:
             raise ValueError("free_start must have one entry")
-    outs, sizes = (seqlens_k, cu_seqlens_q, slots, positions, counts), (n_req, n_req + 1, n_tokens, n_tokens, 3)
-    missing = [n for t, n in zip(outs, sizes) if t is None]
-    if missing:   # one allocation for all of them
-        fresh = iter(torch.empty(sum(missing), dtype=i32, device=dev).split_with_sizes(missing))
-    if len(missing) == 5:
-        outs = tuple(fresh)
-    else:
-        for name, t, n in zip(("seqlens_k", "cu_seqlens_q", "slots", "positions", "counts"), outs, sizes):
-            if t is not None:
-                _dense(t, name, i32, dev)
-                if t.shape != (n,):
-                    raise ValueError(f"{name} must be [{n}], got {list(t.shape)}")
-        outs = tuple(next(fresh) if t is None else t for t in outs)
+    outs = []
+    for name, t, n in (("seqlens_k", seqlens_k, n_req), ("cu_seqlens_q", cu_seqlens_q, n_req + 1), ("slots", slots, n_tokens),
+                       ("positions", positions, n_tokens), ("counts", counts, 3)):
+        if t is None:
+            t = torch.empty(n, dtype=i32, device=dev)
+        else:
+            _dense(t, name, i32, dev)
+            if t.shape != (n,):
+                raise ValueError(f"{name} must be [{n}], got {list(t.shape)}")
+        outs.append(t)
     k, cu, sl, pos, cnt = outs
     rc = lib.sparse_mla_plan_pages(
         seqlens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(), _ptr(free_start),
@@ -474,7 +471,7 @@ def sparse_mla_plan_pages(seqlens, new_lens, block_table, free_pages, n_tokens, 
         table_shape[1], int(page_block), _raw_stream(dev.index))
     if rc != 0:
         raise SmlaError(rc, "sparse_mla_plan_pages")
-    return outs
+    return k, cu, sl, pos, cnt
 
 
 def sparse_mla_append_kv(c_kv, k_pe, slots, kv_pool, norm_weight=None, eps=1e-6, positions=None, rope=None, q_pe=None,

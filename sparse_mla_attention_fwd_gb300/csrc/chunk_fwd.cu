@@ -66,7 +66,7 @@ constexpr int kGens = 4;                  // key buffers, S buffers
 constexpr int kRing = 4;                  // block descriptors ahead
 constexpr int kPairThreads = 288;
 constexpr int kMaxPairs = 80;             // ranges the axis is cut into, at most
-constexpr int kTileCost = 128;            // start and end of a tile, in keys
+constexpr int kTileCost = 256;            // start and end of a tile, in keys
 constexpr int kMinRange = 128;            // shortest range, in keys (at least kKeys)
 constexpr uint32_t kHalfBytes = 16384;    // 32 keys x 256 columns
 constexpr uint32_t kPBytes = 8192;        // 64 rows x 64 keys
@@ -84,7 +84,7 @@ struct ChunkParams {
   __nv_bfloat16* out;
   float* lse;
   float* max_logits;
-  float* part_o;            // [2 pairs][row_cap][512] unnormalised O of a tile's part
+  float* part_o;            // [2 pairs][128 column quads][row_cap][4] unnormalised O of a tile's part
   float* part_stats;        // [2 pairs][3][128]: offset (log2 units), sum, maximum score
   int4* joins;              // [pairs]: first row, rows, last pair of the cut tile that starts there
   int64_t pool_rows, n_req, n_tok;
@@ -431,29 +431,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         uint8_t* put = stage + lane * 64;
         const int put_sw = (lane >> 1) & 3, get_row = lane >> 2;
         const uint8_t* get = stage + get_row * 64 + (((lane & 3) ^ ((get_row >> 1) & 3)) << 4);
-        const bool whole = part < 0;
         // where this lane's 16 bytes of rows get_row, get_row + 8, .. go
-        uint8_t* dst = whole ? reinterpret_cast<uint8_t*>(p.out + (q_row + warp_row + get_row) * kDv + 256 * half)
-                             : reinterpret_cast<uint8_t*>(
-                                   p.part_o + (static_cast<int64_t>(part) * p.row_cap + warp_row + get_row) * kDv + 256 * half);
-        dst += 16 * (lane & 3);
-        const int64_t row_bytes = whole ? kDv * 2 : kDv * 4;
+        uint8_t* dst = reinterpret_cast<uint8_t*>(p.out + (q_row + warp_row + get_row) * kDv + 256 * half) + 16 * (lane & 3);
         const int rows_left = n_rows - warp_row - get_row;
-        auto flush = [&] {
-          __syncwarp();
-#pragma unroll
-          for (int x = 0; x < 4; ++x)   // rows 8 x + get_row; the swizzle repeats every eight rows
-            if (8 * x < rows_left)
-              *reinterpret_cast<uint4*>(dst + 8 * x * row_bytes) = *reinterpret_cast<const uint4*>(get + 512 * x);
-          __syncwarp();
-          dst += 64;
-        };
+        // a part of a tile goes to the workspace as it lies here: four columns of all rows together
+        float4* po = reinterpret_cast<float4*>(p.part_o) + (static_cast<int64_t>(part) * 128 + 64 * half) * p.row_cap + row;
 #pragma unroll 1
         for (int i = 0; i < 8; ++i) {
           uint32_t o[32];
           tmem_ld32(lanes + 32 * i, o);
           tmem_ld_wait();
-          if (whole) {
+          if (part < 0) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               uint32_t v[4];
@@ -464,17 +452,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
               }
               *reinterpret_cast<uint4*>(put + ((j ^ put_sw) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
             }
-            flush();
-          } else {
+            __syncwarp();
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
+            for (int x = 0; x < 4; ++x)   // rows 8 x + get_row; the swizzle repeats every eight rows
+              if (8 * x < rows_left)
+                *reinterpret_cast<uint4*>(dst + 8 * x * (kDv * 2)) = *reinterpret_cast<const uint4*>(get + 512 * x);
+            dst += 64;
+          } else if (live) {
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                *reinterpret_cast<uint4*>(put + ((j ^ put_sw) << 4)) =
-                    make_uint4(o[16 * y + 4 * j], o[16 * y + 4 * j + 1], o[16 * y + 4 * j + 2], o[16 * y + 4 * j + 3]);
-              flush();
-            }
+            for (int j = 0; j < 8; ++j)
+              po[(8 * i + j) * p.row_cap] = make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]),
+                                                        __uint_as_float(o[4 * j + 2]), __uint_as_float(o[4 * j + 3]));
           }
+          __syncwarp();
         }
         // O has been read: the next tile's first PV may overwrite it
         tc_fence_before();
@@ -496,6 +486,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       ++b;
     };
     int4 join = make_int4(0, 0, -1, 0);
+    int64_t join_end = 0;
     bool more = v0 < total && first_req >= 0;
     int64_t start = more ? scan.start : 0;       // the request's position on the axis
     for (int64_t req = first_req; more && req < p.n_req && !stop; ++req) {
@@ -512,13 +503,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
         k = lo;
       }
+      int64_t s = start + p.groups * axis_of(p, r, k);   // the tile's position on the axis
       for (; k < n_tiles && more && !stop; ++k) {
-        const int64_t at = axis_of(p, r, k), size = axis_of(p, r, k + 1) - at;
         const int64_t tok = k * p.tokens_per_tile, last = min(r.n_q, tok + p.tokens_per_tile);
+        const int64_t size = kTileCost + (p.causal ? max(before, static_cast<int64_t>(0)) + last : r.n_k);
         const int64_t key_end = p.causal ? min(max(before + last, static_cast<int64_t>(0)), r.keys) : r.keys;
         const int64_t n_blocks = max((key_end + kKeys - 1) / kKeys, static_cast<int64_t>(1));
-        for (int grp = 0; grp < p.groups && more && !stop; ++grp) {
-          const int64_t s = start + p.groups * at + grp * size;   // the tile's position on the axis
+        for (int grp = 0; grp < p.groups && more && !stop; ++grp, s += size) {
           if (s >= v1) {
             more = false;
             break;
@@ -532,7 +523,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           if (j0 > 0) part = static_cast<int>(2 * pair);
           else if (j1 < n_blocks) {
             part = static_cast<int>(2 * pair + 1);
-            join = make_int4(static_cast<int>(q_row), n_rows, static_cast<int>((s + kKeys * (n_blocks - 1)) / range), 0);
+            join = make_int4(static_cast<int>(q_row), n_rows, 0, 0);
+            join_end = s + kKeys * (n_blocks - 1);   // the tile's last block: in the range of the last pair
           }
           for (int64_t j = j0; j < j1 && !stop; ++j) {
             int32_t pool_row[2];
@@ -572,6 +564,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       }
       start += p.groups * axis_of(p, r, n_tiles);
     }
+    if (join.z == 0) join.z = static_cast<int>(join_end / range);
     acquire();
     if (lane == 0) {
       c.ring[b % kRing].flags = kEnd;
@@ -726,49 +719,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 // ------------------------------------------------------------------------ joining cut tiles
 // A tile cut over pairs w .. w1 left its parts in slots 2w + 1, 2(w+1), .., 2 w1.  With M = max m_i:
 //   l = sum 2^(m_i - M) l_i,   O = sum 2^(m_i - M) O_i / (l + [sink] 2^(sink log2 e - M)).
-constexpr int kJoinRows = 4;
-constexpr int kJoinThreads = 128 * kJoinRows;   // four value columns a thread
+// A CTA takes 32 rows and 128 columns, a lane a row: the parts are read as they were written, 16 bytes of 32
+// rows at a time, and the output leaves through shared memory in whole row pieces.
+constexpr int kJoinRows = 32;
+constexpr int kJoinThreads = 256;
 
 __global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const ChunkParams p) {
+  __shared__ __align__(16) uint2 tile[kJoinRows][33];   // four columns each; padded against bank conflicts
   const int w = blockIdx.x;
   cudaGridDependencySynchronize();
   const int4 join = p.joins[w];
-  const int row = blockIdx.y * kJoinRows + (threadIdx.x >> 7), t = threadIdx.x & 127;
-  if (join.z < 0 || row >= join.y) return;
+  const int row0 = blockIdx.y * kJoinRows;
+  if (join.z < 0 || row0 >= join.y) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = row0 + lane;
+  const int col4 = 32 * blockIdx.z + 4 * warp;          // four column quads of this warp
+  const bool live = row < join.y;
   auto slot = [&](int i) { return i == w ? 2 * w + 1 : 2 * i; };
-  float M = -INFINITY, top = -INFINITY;
-  for (int i = w; i <= join.z; ++i) {
-    const float* st = p.part_stats + slot(i) * 3 * 128 + row;
-    M = fmaxf(M, st[0]);
-    top = fmaxf(top, st[256]);
-  }
-  float l = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (M > -INFINITY) {
+  const float* stats = p.part_stats + row;
+  float M = -INFINITY, top = -INFINITY, l = 0.f;
+  float4 acc[4] = {};
+  if (live) {
 #pragma unroll 4
+    for (int i = w; i <= join.z; ++i) M = fmaxf(M, stats[slot(i) * 3 * 128]);
+    const float base = M > -INFINITY ? M : 0.f;
+#pragma unroll 2
     for (int i = w; i <= join.z; ++i) {
-      const float* st = p.part_stats + slot(i) * 3 * 128 + row;
-      const float4 o = reinterpret_cast<const float4*>(p.part_o + (static_cast<int64_t>(slot(i)) * p.row_cap + row) * kDv)[t];
-      const float a = exp2f(st[0] - M);
+      const float* st = stats + slot(i) * 3 * 128;
+      const float4* o = reinterpret_cast<const float4*>(p.part_o) + (static_cast<int64_t>(slot(i)) * 128 + col4) * p.row_cap + row;
+      const float a = exp2f(st[0] - base);
       l = fmaf(a, st[128], l);
-      acc.x = fmaf(a, o.x, acc.x);
-      acc.y = fmaf(a, o.y, acc.y);
-      acc.z = fmaf(a, o.z, acc.z);
-      acc.w = fmaf(a, o.w, acc.w);
+      top = fmaxf(top, st[256]);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const float4 v = o[x * p.row_cap];
+        acc[x].x = fmaf(a, v.x, acc[x].x);
+        acc[x].y = fmaf(a, v.y, acc[x].y);
+        acc[x].z = fmaf(a, v.z, acc[x].z);
+        acc[x].w = fmaf(a, v.w, acc[x].w);
+      }
     }
   }
   const bool empty = !(l > 0.f);
   const int64_t r = static_cast<int64_t>(join.x) + row;
   float den = l;
-  if (p.attn_sink && !empty) den += exp2f(fmaf(__ldg(p.attn_sink + r % p.h_q), kLog2e, -M));
+  if (p.attn_sink && live && !empty) den += exp2f(fmaf(__ldg(p.attn_sink + r % p.h_q), kLog2e, -M));
   const float inv = empty ? 0.f : 1.f / den;
-  uint2 v = make_uint2(0u, 0u);
-  if (!empty) v = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-  reinterpret_cast<uint2*>(p.out + r * kDv)[t] = v;
-  if (t == 0) {
+#pragma unroll
+  for (int x = 0; x < 4; ++x)
+    tile[lane][4 * warp + x] = empty ? make_uint2(0u, 0u)
+                                     : make_uint2(pack_bf16x2(acc[x].x * inv, acc[x].y * inv),
+                                                  pack_bf16x2(acc[x].z * inv, acc[x].w * inv));
+  if (live && warp == 0 && blockIdx.z == 0) {
     p.lse[r] = empty ? INFINITY : (M + log2f(l)) * kLn2;
     p.max_logits[r] = empty ? -INFINITY : top;
   }
+  __syncthreads();
+  for (int k = warp; k < kJoinRows && row0 + k < join.y; k += kJoinThreads / 32)
+    reinterpret_cast<uint2*>(p.out + (static_cast<int64_t>(join.x) + row0 + k) * kDv + 128 * blockIdx.z)[lane] = tile[k][lane];
 }
 
 // ------------------------------------------------------------------------ host side
@@ -840,7 +847,7 @@ smla_status launch(const CUtensorMap& qm, const CUtensorMap& hm, const CUtensorM
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(pairs, (p.row_cap + kJoinRows - 1) / kJoinRows);
+  cfg.gridDim = dim3(pairs, (p.row_cap + kJoinRows - 1) / kJoinRows, kDv / 128);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cfg.attrs = &early;
