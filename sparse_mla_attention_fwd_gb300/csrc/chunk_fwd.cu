@@ -64,7 +64,7 @@ constexpr int kTileRows = 128;            // rows of a tile, 64 per CTA
 constexpr int kKeys = 64;                 // keys of a block, 32 per CTA
 constexpr int kGens = 4;                  // key buffers, S buffers
 constexpr int kRing = 4;                  // block descriptors ahead
-constexpr int kPairThreads = 288;
+constexpr int kPairThreads = 416;
 constexpr int kMaxPairs = 80;             // ranges the axis is cut into, at most
 constexpr int kTileCost = 256;            // start and end of a tile, in keys
 constexpr int kMinRange = 128;            // shortest range, in keys (at least kKeys)
@@ -72,7 +72,8 @@ constexpr uint32_t kHalfBytes = 16384;    // 32 keys x 256 columns
 constexpr uint32_t kPBytes = 8192;        // 64 rows x 64 keys
 constexpr uint32_t kTmemCols = 512, kTmemS = 256;
 
-enum : uint32_t { kFirst = 1u, kLast = 2u, kEnd = 4u, kDense = 8u };
+enum : uint32_t { kFirst = 1u, kLast = 2u, kEnd = 4u };
+constexpr uint32_t kTileBar = 3;          // named barriers 1, 2: softmax warps that share rows; 3, 4: a tile is done
 
 __device__ int g_chunk_status = 0;        // SMLA_ERR_DEVICE_TIMEOUT once any wait gave up
 
@@ -90,7 +91,8 @@ struct ChunkParams {
   int64_t pool_rows, n_req, n_tok;
   float sm_scale;
   int h_q, max_blocks, page_block, causal;
-  int box;                  // rows of a tiled load: power of two that divides page_block, or 0
+  int box;                  // rows of a tiled load: 32, 16 or 8, a divisor of page_block; or 0
+  int pool_end;             // first row behind the pool
   int tokens_per_tile, groups;   // 128 / h_q and 1, or 1 and the 128-head groups of a token
   int row_cap;
 };
@@ -137,8 +139,11 @@ struct __align__(16) BlockDesc {
 
 struct Control {
   BlockDesc ring[kRing];
-  float ex[2][128];      // row maxima of the two key halves
-  float sum[128];
+  float ex[2][128];      // row maxima (at a tile's end row sums) of the two key halves
+  float inv[2][64];      // a finished tile's factor of each row, 0 for an empty row; by tile parity
+  struct {
+    int32_t q_row, n_rows, part, last;   // last: the tile's last block, or -1 behind the last tile
+  } done[2];
   uint64_t ring_full[kRing], ring_empty[kRing];
   uint64_t k_full[kGens], x_full[kGens];      // both CTAs' keys / foreign halves have landed (first CTA)
   uint64_t s_full[kGens], pv_done[kGens];     // S computed / PV done (both CTAs)
@@ -164,29 +169,56 @@ struct Smem {
 };
 static_assert(Smem<576>::kBytes <= 232448, "a CTA's shared memory");
 
+// Lane i of four neighbours holds pieces 0-3 of row i; afterwards piece i of rows 0-3.
+__device__ __forceinline__ void transpose_4x4(uint32_t (&v)[4][4], int lane) {
+  const bool hi2 = lane & 2, hi1 = lane & 1;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, hi2 ? v[x][w] : v[x + 2][w], 2);
+      if (hi2) v[x][w] = got;
+      else v[x + 2][w] = got;
+    }
+#pragma unroll
+    for (int x = 0; x < 4; x += 2) {
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, hi1 ? v[x][w] : v[x + 1][w], 1);
+      if (hi1) v[x][w] = got;
+      else v[x + 1][w] = got;
+    }
+  }
+}
+
 // ------------------------------------------------------------------------ bounded waits
 __device__ __forceinline__ void give_up(volatile int* abort) {
   *abort = 1;
   atomicExch(&g_chunk_status, static_cast<int>(SMLA_ERR_DEVICE_TIMEOUT));
 }
 
+// A waiting thread sleeps on the barrier rather than polling it: the polls of a dozen warps take shared-memory
+// cycles from the tensor unit's operands.
+template <bool PAIR>
+__device__ __forceinline__ void wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  constexpr uint32_t kSleepNs = 100000;
+  const uint32_t a = smem_u32(bar);
+  auto done = [&] { return PAIR ? mbar_sleep_cluster(a, parity, kSleepNs) : mbar_sleep(a, parity, kSleepNs); };
+  if (done()) return;
+  const uint64_t t0 = globaltimer_ns();
+  uint32_t spins = 0;
+  while (!done()) {
+    if ((++spins & 15u) == 0u && (*abort || globaltimer_ns() - t0 > kWaitLimitNs)) return give_up(abort);
+  }
+}
 __device__ __forceinline__ void wait_on(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  if (!mbar_wait_bounded(smem_u32(bar), parity, abort, kWaitLimitNs)) give_up(abort);
+  wait_bounded<false>(bar, parity, abort);
+}
+// For a barrier on which the other CTA's threads arrive.
+__device__ __forceinline__ void wait_on_pair(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  wait_bounded<true>(bar, parity, abort);
 }
 
 // Whether a wait of this CTA has given up, agreed on by the warp.
 __device__ __forceinline__ bool stopped(volatile int* abort) { return __any_sync(0xffffffffu, *abort != 0); }
-
-// The same for a barrier on which the other CTA's threads arrive.
-__device__ __forceinline__ void wait_on_pair(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  const uint32_t b = smem_u32(bar);
-  if (mbar_try_wait_cluster(b, parity)) return;
-  const uint64_t t0 = globaltimer_ns();
-  for (uint32_t spins = 1;; ++spins) {
-    if (mbar_try_wait_cluster(b, parity)) return;
-    if ((spins & 63u) == 0u && (*abort || globaltimer_ns() - t0 > kWaitLimitNs)) return give_up(abort);
-  }
-}
 
 __device__ __forceinline__ int64_t pair_scan(int64_t v, int64_t* warp_sum) {   // inclusive, over the CTA
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -204,8 +236,8 @@ __device__ __forceinline__ int64_t pair_scan(int64_t v, int64_t* warp_sum) {   /
 template <int D_QK>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     chunk_fwd_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap half_map,
-                     const __grid_constant__ CUtensorMap box_map, const __grid_constant__ CUtensorMap row_map,
-                     const ChunkParams p) {
+                     const __grid_constant__ CUtensorMap box_map, const __grid_constant__ CUtensorMap group_map,
+                     const __grid_constant__ CUtensorMap row_map, const ChunkParams p) {
   using L = Smem<D_QK>;
   constexpr int kChunks = L::kChunks;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -245,6 +277,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     prefetch_map(&q_map);
     prefetch_map(&half_map);
     prefetch_map(&box_map);
+    prefetch_map(&group_map);
     prefetch_map(&row_map);
   }
   tc_fence_before();
@@ -297,18 +330,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const int64_t first_req = scan.req;
 
   if (warp >= 4 && warp < 8) {
-    // ============================================================ softmax, rescaling, epilogue
+    // ============================================================ softmax and rescaling
     const int t = tid - 128;                       // TMEM lane
     const int row = (t & 63) + 64 * static_cast<int>(rank);
     const int half = t >> 6;                       // keys and value columns of this lane
     const uint32_t lanes = tmem + (static_cast<uint32_t>(t & 96) << 16);
     const uint32_t bar_id = 1 + ((t >> 5) & 1);    // the two warps that share rows
     const float scale2 = p.sm_scale * kLog2e;
-    const uint32_t p_full = map_to_rank(smem_u32(&c.p_full), 0), o_free = map_to_rank(smem_u32(&c.o_free), 0);
+    const uint32_t p_full = map_to_rank(smem_u32(&c.p_full), 0);
     uint8_t* p_row = s_p + (t & 63) * 128;
     const int sw = t & 7;
     float m = -INFINITY, top = -INFINITY, l = 0.f;   // exponent offset (log2 units), max of q.k, sum
-    int b = 0;
+    int b = 0, tile = 0;
     int limit = 0;                                   // first key position this row does not see
     // The two warps that share rows meet at one barrier in every round, the last one included, and leave
     // together, also when a wait gave up.
@@ -399,9 +432,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       if (lane == 0) mbar_arrive_pair(p_full);
 
       if (flags & kLast) {
-        c.sum[t] = l;
+        // l of both key halves; the barrier behind it keeps the next block's maxima off these slots
+        c.ex[(b + 1) & 1][t] = l;
         named_bar_sync(bar_id, 64);
-        l += c.sum[t ^ 64];
+        l += c.ex[(b + 1) & 1][t ^ 64];
+        named_bar_sync(bar_id, 64);
         const bool empty = !(l > 0.f);
         const bool live = row < n_rows;
         float inv = 1.f;
@@ -420,59 +455,78 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           st[128] = empty ? 0.f : l;
           st[256] = empty ? -INFINITY : top * p.sm_scale;
         }
-        wait_on(&c.pv_done[g], (b / kGens) & 1, abort);
-        __syncwarp();
-        tc_fence_after();
-        // A lane holds a row's 256 values; stored as they are, each store instruction would touch 32
-        // rows.  They go through the warp's quarter of the P tile (PV has read it), 64 bytes of 32
-        // rows at a time, and leave with four lanes a row.
-        const int warp_row = row - lane;   // the warp's first row of the tile
-        uint8_t* stage = s_p + (t >> 5) * 2048;
-        uint8_t* put = stage + lane * 64;
-        const int put_sw = (lane >> 1) & 3, get_row = lane >> 2;
-        const uint8_t* get = stage + get_row * 64 + (((lane & 3) ^ ((get_row >> 1) & 3)) << 4);
-        // where this lane's 16 bytes of rows get_row, get_row + 8, .. go
-        uint8_t* dst = reinterpret_cast<uint8_t*>(p.out + (q_row + warp_row + get_row) * kDv + 256 * half) + 16 * (lane & 3);
-        const int rows_left = n_rows - warp_row - get_row;
-        // a part of a tile goes to the workspace as it lies here: four columns of all rows together
-        float4* po = reinterpret_cast<float4*>(p.part_o) + (static_cast<int64_t>(part) * 128 + 64 * half) * p.row_cap + row;
-#pragma unroll 1
-        for (int i = 0; i < 8; ++i) {
-          uint32_t o[32];
-          tmem_ld32(lanes + 32 * i, o);
-          tmem_ld_wait();
-          if (part < 0) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t v[4];
-#pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                const float a = __uint_as_float(o[8 * j + 2 * x]), e = __uint_as_float(o[8 * j + 2 * x + 1]);
-                v[x] = empty ? 0u : pack_bf16x2(a * inv, e * inv);
-              }
-              *reinterpret_cast<uint4*>(put + ((j ^ put_sw) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
-            }
-            __syncwarp();
-#pragma unroll
-            for (int x = 0; x < 4; ++x)   // rows 8 x + get_row; the swizzle repeats every eight rows
-              if (8 * x < rows_left)
-                *reinterpret_cast<uint4*>(dst + 8 * x * (kDv * 2)) = *reinterpret_cast<const uint4*>(get + 512 * x);
-            dst += 64;
-          } else if (live) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              po[(8 * i + j) * p.row_cap] = make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]),
-                                                        __uint_as_float(o[4 * j + 2]), __uint_as_float(o[4 * j + 3]));
-          }
-          __syncwarp();
+        // The epilogue warps take it from here.  Two slots are enough: this group's next tile but one comes
+        // behind PV of its next tile, which waits until they have read O of this one.
+        if (half == 0) c.inv[tile & 1][t] = inv;
+        if (t == 0) {
+          c.done[tile & 1].q_row = static_cast<int32_t>(q_row);
+          c.done[tile & 1].n_rows = n_rows;
+          c.done[tile & 1].part = part;
+          c.done[tile & 1].last = b;
         }
-        // O has been read: the next tile's first PV may overwrite it
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_pair(o_free);
+        named_bar_arrive(kTileBar + (tile & 1), 256);
+        ++tile;
       }
     }
-  } else if (warp == 0) {
+    // PV of the last tile has waited for the epilogue of the one before, whose slot the end takes
+    if (b > 0) wait_on(&c.pv_done[(b - 1) % kGens], ((b - 1) / kGens) & 1, abort);
+    if (t == 0) c.done[tile & 1].last = -1;
+    __syncwarp();
+    named_bar_arrive(kTileBar + (tile & 1), 256);
+  } else if (warp >= 8 && warp < 12) {
+    // ============================================================ epilogue
+    const int t = tid - 256, row = (t & 63) + 64 * static_cast<int>(rank), half = t >> 6;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(t & 96) << 16);
+    const uint32_t o_free = map_to_rank(smem_u32(&c.o_free), 0);
+    for (int tile = 0;; ++tile) {
+      const auto& d = c.done[tile & 1];
+      named_bar_sync(kTileBar + (tile & 1), 256);   // the softmax warps arrive for each tile and for the end
+      const int last = d.last, n_rows = d.n_rows, part = d.part;
+      if (last < 0) break;
+      const int64_t q_row = d.q_row;
+      const float inv = c.inv[tile & 1][t & 63];
+      wait_on(&c.pv_done[last % kGens], (last / kGens) & 1, abort);
+      __syncwarp();
+      tc_fence_after();
+      // A lane holds a row's 256 values; stored as they are, each store instruction would touch 32 rows.
+      // Four lanes exchange their rows' pieces of 64 bytes first, so that each store covers 64 bytes of
+      // eight rows.  A part of a tile goes to the workspace as it lies here: four columns of all rows
+      // together.
+      const int row4 = row - (lane & 3);
+      __nv_bfloat16* out = p.out + (q_row + row4) * kDv + 256 * half + 8 * (lane & 3);
+      float4* po = reinterpret_cast<float4*>(p.part_o) + (static_cast<int64_t>(part) * 128 + 64 * half) * p.row_cap + row;
+#pragma unroll 1
+      for (int i = 0; i < 8; ++i) {
+        uint32_t o[32];
+        tmem_ld32(lanes + 32 * i, o);
+        tmem_ld_wait();
+        if (part < 0) {
+          uint32_t v[4][4];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float a = __uint_as_float(o[2 * j]), e = __uint_as_float(o[2 * j + 1]);
+            v[j >> 2][j & 3] = inv == 0.f ? 0u : pack_bf16x2(a * inv, e * inv);
+          }
+          transpose_4x4(v, lane);
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (row4 + x < n_rows)
+              *reinterpret_cast<uint4*>(out + x * kDv + 32 * i) = make_uint4(v[x][0], v[x][1], v[x][2], v[x][3]);
+        } else if (row < n_rows) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            po[(8 * i + j) * p.row_cap] = make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]),
+                                                      __uint_as_float(o[4 * j + 2]), __uint_as_float(o[4 * j + 3]));
+        }
+        __syncwarp();
+      }
+      // O has been read: the next tile's first PV may overwrite it
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_pair(o_free);
+    }
+  } else {
+    if (warp == 0) {
     // ============================================================ scheduler
     int b = 0;
     bool stop = false;
@@ -549,8 +603,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             if (lane == 0) {
               d.mask[0] = mask[0];
               d.mask[1] = mask[1];
-              d.flags = (j == j0 ? kFirst : 0u) | (j == j1 - 1 ? kLast : 0u) |
-                        (p.box > 0 && (mask[0] & mask[1]) == 0xffffffffu ? kDense : 0u);
+              d.flags = (j == j0 ? kFirst : 0u) | (j == j1 - 1 ? kLast : 0u);
               d.key0 = static_cast<int32_t>(kKeys * j);
               d.q_row = static_cast<int32_t>(q_row);
               d.n_rows = n_rows;
@@ -572,38 +625,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
     publish();
   } else if (warp == 1 || warp == 2) {
-    // ============================================================ loads
-    // Warp 1: all columns of the CTA's own 32 keys.  Warp 2: Q at a tile's start, and the CTA's value
-    // columns of the other CTA's 32 keys.  Blocks whose 64 keys all count go by tiled loads: 32 rows
-    // of four 64-column chunks at once where pages allow it, else boxes of 8 or 16 rows of a chunk.
-    // One elected thread issues them: issued from several lanes, each load costs the warp a turn.  Any
-    // other block goes by row gathers, where a key that does not count has row -1 and reads as zeros.
+    // ============================================================ key loads
+    // Warp 1: all columns of the CTA's own 32 keys.  Warp 2: the CTA's value columns of the other CTA's 32
+    // keys, in place of the foreign half, and each tile's Q, as soon as S of the tile before is done.  One elected thread issues the loads: issued from several lanes,
+    // each costs the warp a turn.
     const bool foreign = warp == 2;
     const uint32_t k_full = map_to_rank(smem_u32(&c.k_full[0]), 0), x_full = map_to_rank(smem_u32(&c.x_full[0]), 0);
     const uint32_t q_full = map_to_rank(smem_u32(&c.q_full), 0);
-    const int keys0 = 32 * static_cast<int>(foreign ? 1 - rank : rank);   // the keys of the block that this warp loads
-    // four 64-column chunks from chunk0 on go to dst, the rope chunk to `rope` (if not 0)
-    auto load = [&](const BlockDesc& d, bool dense, int chunk0, uint32_t dst, uint32_t rope, uint32_t bar) {
-      if (dense) {
-        if (elect_one()) {
-          if (p.box == 32) {
-            const int row = d.rows[keys0];
-            tma_load_3d_pair(dst, &half_map, 0, row, chunk0, bar);
-            if (rope) tma_load_2d_pair(rope, &box_map, 512, row, bar);
+    const int which = static_cast<int>(foreign ? 1 - rank : rank);   // the half of the block's keys that this warp loads
+    // n_chunks 64-column chunks from chunk0 on, 4096 bytes each.  32 keys that all count go by tiled loads,
+    // four chunks at once where they lie in one page.  Otherwise groups of eight rows go by tiled loads where
+    // all eight keys count, or none (a group behind the pool's end reads as zeros), and mixed groups row by
+    // row (row -1 reads as zeros).
+    auto load = [&](const BlockDesc& d, int chunk0, int n_chunks, uint32_t dst, uint32_t bar) {
+      const uint32_t mask = d.mask[which];
+      const int32_t* rows = d.rows + 32 * which;
+      if (p.box == 32 && mask == 0xffffffffu && n_chunks == 4) {
+        tma_load_3d_pair(dst, &half_map, 0, rows[0], chunk0, bar);
+      } else if (p.box > 0 && mask == 0xffffffffu) {
+        for (int k0 = 0; k0 < 32; k0 += p.box)
+          for (int ch = 0; ch < n_chunks; ++ch)
+            tma_load_2d_pair(dst + ch * 4096 + k0 * 128, &box_map, 64 * (chunk0 + ch), rows[k0], bar);
+      } else {
+        for (int k0 = 0; k0 < 32; k0 += 8, rows += 8, dst += 1024) {
+          const uint32_t group = (mask >> k0) & 0xffu;
+          if (p.box > 0 && (group == 0u || group == 0xffu)) {
+            const int row = group ? rows[0] : p.pool_end;
+            for (int ch = 0; ch < n_chunks; ++ch)
+              tma_load_2d_pair(dst + ch * 4096, &group_map, 64 * (chunk0 + ch), row, bar);
           } else {
-            for (int k0 = 0; k0 < 32; k0 += p.box) {
-              const int row = d.rows[keys0 + k0];
-              for (int ch = 0; ch < 4; ++ch)
-                tma_load_2d_pair(dst + ch * 4096 + k0 * 128, &box_map, 64 * (chunk0 + ch), row, bar);
-              if (rope) tma_load_2d_pair(rope + k0 * 128, &box_map, 512, row, bar);
+            for (int x = 0; x < 8; x += 4) {
+              const int4 rr = *reinterpret_cast<const int4*>(rows + x);
+              for (int ch = 0; ch < n_chunks; ++ch)
+                tma_gather4_pair(dst + ch * 4096 + x * 128, &row_map, 64 * (chunk0 + ch), rr.x, rr.y, rr.z, rr.w, bar);
             }
           }
         }
-      } else {
-        const int k0 = 4 * (lane & 7), ch = lane >> 3;   // eight groups of four rows, four chunks
-        const int4 rr = *reinterpret_cast<const int4*>(&d.rows[keys0 + k0]);
-        tma_gather4_pair(dst + ch * 4096 + k0 * 128, &row_map, 64 * (chunk0 + ch), rr.x, rr.y, rr.z, rr.w, bar);
-        if (rope && lane < 8) tma_gather4_pair(rope + k0 * 128, &row_map, 512, rr.x, rr.y, rr.z, rr.w, bar);
+      }
+    };
+    auto load_q = [&](const BlockDesc& d) {
+      if (elect_one()) {
+        if (rank == 0) mbar_arrive_expect_tx(smem_u32(&c.q_full), 2 * L::kQBytes);
+        const int q_row = d.q_row + 64 * static_cast<int>(rank);
+        for (int ch = 0; ch < kChunks; ++ch) tma_load_2d_pair(smem_u32(s_q + ch * 8192), &q_map, 64 * ch, q_row, q_full);
       }
       __syncwarp();
     };
@@ -614,28 +678,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       if (stopped(abort)) break;
       const uint32_t flags = d.flags;
       if (flags & kEnd) break;
-      const bool dense = (flags & kDense) != 0;
       const uint32_t gen = smem_u32(s_kv) + g * L::kGenBytes;
       if (foreign) {
-        if (flags & kFirst) {   // this warp has seen S of every earlier block done: Q is free
-          if (elect_one()) {
-            if (rank == 0) mbar_arrive_expect_tx(smem_u32(&c.q_full), 2 * L::kQBytes);
-            const int row = d.q_row + 64 * static_cast<int>(rank);
-            for (int ch = 0; ch < kChunks; ++ch) tma_load_2d_pair(smem_u32(s_q + ch * 8192), &q_map, 64 * ch, row, q_full);
-          }
-          __syncwarp();
-        }
-        wait_on(&c.s_full[g], (b / kGens) & 1, abort);   // S has read the foreign half
+        if (b == 0) load_q(d);
+        wait_on(&c.s_full[g], (b / kGens) & 1, abort);   // S has read the foreign half, and at a tile's end Q
         if (stopped(abort)) break;
-        if (rank == 0 && lane == 0) mbar_arrive_expect_tx(smem_u32(&c.x_full[g]), 2 * kHalfBytes);
-        load(d, dense, 4 * static_cast<int>(rank), gen + (1 - rank) * kHalfBytes, 0u, x_full + 8 * g);
+        if (flags & kLast) {
+          const BlockDesc& next = c.ring[(b + 1) % kRing];
+          wait_on(&c.ring_full[(b + 1) % kRing], ((b + 1) / kRing) & 1, abort);
+          if (stopped(abort)) break;
+          if (!(next.flags & kEnd)) load_q(next);
+        }
+        if (elect_one()) {
+          if (rank == 0) mbar_arrive_expect_tx(smem_u32(&c.x_full[g]), 2 * kHalfBytes);
+          load(d, 4 * static_cast<int>(rank), 4, gen + (1 - rank) * kHalfBytes, x_full + 8 * g);
+        }
       } else {
         if (b >= kGens) wait_on(&c.pv_done[g], ((b / kGens) - 1) & 1, abort);
         if (stopped(abort)) break;
-        if (rank == 0 && lane == 0) mbar_arrive_expect_tx(smem_u32(&c.k_full[g]), 2 * L::kGenBytes);
-        load(d, dense, 0, gen, kChunks > 8 ? gen + 2 * kHalfBytes : 0u, k_full + 8 * g);
-        load(d, dense, 4, gen + kHalfBytes, 0u, k_full + 8 * g);
+        if (elect_one()) {
+          const uint32_t bar = k_full + 8 * g;
+          if (rank == 0) mbar_arrive_expect_tx(smem_u32(&c.k_full[g]), 2 * L::kGenBytes);
+          load(d, 0, 4, gen, bar);
+          load(d, 4, 4, gen + kHalfBytes, bar);
+          if constexpr (kChunks > 8) load(d, 8, 1, gen + 2 * kHalfBytes, bar);
+        }
       }
+      __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&c.ring_empty[b % kRing]));
     }
   } else if (warp == 3 && rank == 0) {
@@ -663,7 +732,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 8 && rank == 0) {
+  } else if (warp == 12 && rank == 0) {
     // ============================================================ PV issuer
     if (elect_one()) {
       constexpr uint32_t idesc = make_idesc_bf16(kTileRows, 256, false, true);
@@ -696,6 +765,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       }
     }
     __syncwarp();
+  }
   }
 
   // ---- every copy and product has been waited for (each tile's epilogue follows its last PV) unless a
@@ -792,21 +862,31 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// Boxes of box_rows rows x box_chunks chunks of 64 columns of a row-major bf16 matrix, chunk after chunk, 128-byte
-// swizzle.  One chunk: a 2-D map, addressed by column and row; more: 3-D, by 0, row and chunk.
-bool make_map(CUtensorMap* m, const void* base, int64_t rows, int cols, int box_rows, int box_chunks = 1) {
+bool encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+            const cuuint32_t* box) {
   const auto fn = encode_fn();
   if (!fn) return false;
+  const cuuint32_t es[3] = {1, 1, 1};
   std::memset(m, 0, sizeof(*m));
-  const cuuint64_t pitch = static_cast<cuuint64_t>(cols) * 2;
-  const bool flat = box_chunks == 1;
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(flat ? cols : 64), static_cast<cuuint64_t>(rows),
-                              static_cast<cuuint64_t>(cols / 64)};
-  const cuuint64_t strides[2] = {pitch, 128};
-  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(box_chunks)}, es[3] = {1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, flat ? 2 : 3, const_cast<void*>(base), dims, strides, box, es,
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// box_rows rows of 64 columns of a row-major bf16 matrix, addressed by column and row; 128-byte swizzle.
+bool map_rows(CUtensorMap* m, const void* base, int64_t rows, int cols, int box_rows) {
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
+  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
+  return encode(m, base, 2, dims, strides, box);
+}
+
+// The same by (column in its chunk of 64, row, chunk): 32 rows of four chunks, chunk after chunk.
+bool map_half(CUtensorMap* m, const void* base, int64_t rows, int cols) {
+  const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(cols / 64)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * 2, 128};
+  const cuuint32_t box[3] = {64, 32, 4};
+  return encode(m, base, 3, dims, strides, box);
 }
 
 struct Workspace {
@@ -838,9 +918,9 @@ int device_sms() {
 }
 
 template <int D_QK>
-smla_status launch(const CUtensorMap& qm, const CUtensorMap& hm, const CUtensorMap& bm, const CUtensorMap& rm,
-                   const ChunkParams& p, int pairs, cudaStream_t stream) {
-  chunk_fwd_kernel<D_QK><<<2 * pairs, kPairThreads, Smem<D_QK>::kBytes, stream>>>(qm, hm, bm, rm, p);
+smla_status launch(const CUtensorMap& qm, const CUtensorMap& hm, const CUtensorMap& bm, const CUtensorMap& gm,
+                   const CUtensorMap& rm, const ChunkParams& p, int pairs, cudaStream_t stream) {
+  chunk_fwd_kernel<D_QK><<<2 * pairs, kPairThreads, Smem<D_QK>::kBytes, stream>>>(qm, hm, bm, gm, rm, p);
   if (cudaGetLastError() != cudaSuccess) return SMLA_ERR_LAUNCH;
   // the joining kernel's CTAs come up while the first one still runs, and wait for its end
   cudaLaunchAttribute early{};
@@ -910,18 +990,20 @@ smla_status sparse_mla_chunk_fwd_paged(const void* q, const void* kv_pool, int64
   p.max_blocks = max_blocks;
   p.page_block = page_block;
   p.causal = causal != 0;
-  // boxes of 8 rows and more keep the 128-byte swizzle's 8-row pattern; smaller pages go by gathers
+  // tiled loads take rows of one page, in groups of eight (the 128-byte swizzle's pattern)
   p.box = page_block % 32 == 0 ? 32 : page_block % 16 == 0 ? 16 : page_block % 8 == 0 ? 8 : 0;
+  p.pool_end = static_cast<int>(pool_rows);
   p.tokens_per_tile = h_q <= kTileRows ? kTileRows / h_q : 1;
   p.groups = h_q <= kTileRows ? 1 : (h_q + kTileRows - 1) / kTileRows;
   p.row_cap = static_cast<int>(n_tok * h_q < kTileRows ? n_tok * h_q : kTileRows);
-  CUtensorMap qm, hm, bm, rm;
-  if (!make_map(&qm, q, n_tok * h_q, d_qk, 64) || !make_map(&hm, kv_pool, pool_rows, d_qk, 32, 4) ||
-      !make_map(&bm, kv_pool, pool_rows, d_qk, p.box ? p.box : 8) || !make_map(&rm, kv_pool, pool_rows, d_qk, 1))
+  CUtensorMap qm, hm, bm, gm, rm;
+  if (!map_rows(&qm, q, n_tok * h_q, d_qk, 64) || !map_half(&hm, kv_pool, pool_rows, d_qk) ||
+      !map_rows(&bm, kv_pool, pool_rows, d_qk, p.box ? p.box : 8) || !map_rows(&gm, kv_pool, pool_rows, d_qk, 8) ||
+      !map_rows(&rm, kv_pool, pool_rows, d_qk, 1))
     return SMLA_ERR_TENSOR_MAP;
   const int pairs = sms / 2 < kMaxPairs ? sms / 2 : kMaxPairs;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return d_qk == 512 ? launch<512>(qm, hm, bm, rm, p, pairs, s) : launch<576>(qm, hm, bm, rm, p, pairs, s);
+  return d_qk == 512 ? launch<512>(qm, hm, bm, gm, rm, p, pairs, s) : launch<576>(qm, hm, bm, gm, rm, p, pairs, s);
 }
 
 smla_status sparse_mla_chunk_device_status(int reset) {
