@@ -116,13 +116,24 @@ __device__ __forceinline__ int64_t token_tiles(const ChunkParams& p, const Reque
   return (static_cast<uint32_t>(r.n_q) + p.tokens_per_tile - 1u) / static_cast<uint32_t>(p.tokens_per_tile);
 }
 
-// Axis length of the first k token tiles of a request (one head group).  A tile's own length is at
-// least its keys: with fewer keys than tokens the axis counts the tokens.
-__device__ __forceinline__ int64_t axis_of(const ChunkParams& p, const Request& r, int64_t k) {
-  if (!p.causal) return k * (r.n_k + kTileCost);
-  const int64_t base = max(r.n_k - r.n_q, static_cast<int64_t>(0)), n = token_tiles(p, r), t = p.tokens_per_tile;
+// Axis length of the first k token tiles of a request.  A tile's own length is at least its keys: with fewer
+// keys than tokens the axis counts the tokens.
+__device__ __forceinline__ int64_t axis_of(const ChunkParams& p, const Request& r, int64_t k, int64_t n) {
+  if (!p.causal) return p.groups * k * (r.n_k + kTileCost);
+  const int64_t base = max(r.n_k - r.n_q, static_cast<int64_t>(0)), t = p.tokens_per_tile;
   const int64_t ends = k < n ? t * (k * (k + 1) / 2) : t * (n * (n - 1) / 2) + r.n_q;   // sum of min(n_q, (i + 1) t)
-  return k * (base + kTileCost) + (k > 0 ? ends : 0);
+  return p.groups * (k * (base + kTileCost) + (k > 0 ? ends : 0));
+}
+__device__ __forceinline__ int64_t axis_of(const ChunkParams& p, const Request& r) {   // the whole request
+  const int64_t n = token_tiles(p, r);
+  return axis_of(p, r, n, n);
+}
+
+// Length of a pair's range.
+__device__ __forceinline__ int64_t range_of(int64_t total, int64_t pairs) {
+  const int64_t up = total + pairs - 1;
+  const int64_t each = up <= UINT32_MAX ? static_cast<uint32_t>(up) / static_cast<uint32_t>(pairs) : up / pairs;
+  return max(each, static_cast<int64_t>(kMinRange));
 }
 
 // ------------------------------------------------------------------------ shared memory
@@ -154,7 +165,7 @@ struct Control {
 
 struct RangeScan {       // lies in the P tile until the first P is written
   int64_t warp_sum[kPairThreads / 32];
-  int64_t total;
+  int64_t total, run;
   int64_t req, start;    // request in which this pair's range starts, its position on the axis
 };
 
@@ -283,51 +294,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   tc_fence_before();
   __syncwarp();
   cluster_arrive();   // barriers and tensor memory of this CTA are ready
-  // This pair's range of the axis: the requests' lengths summed, then the request found in which the
-  // range starts (from the same sums when each thread has one request at most).
+  // The scheduler finds this pair's range of the axis.  With 32 requests at most its warp does so alone;
+  // with more, the CTA's threads sum the requests' lengths and find the request in which the range
+  // starts (from the same sums when each thread has one request at most).
   RangeScan& scan = *reinterpret_cast<RangeScan*>(s_p);
-  int64_t mine = 0;
-  for (int64_t b = tid; b < p.n_req; b += kPairThreads) {
-    const Request r = request(p, b);
-    mine += p.groups * axis_of(p, r, token_tiles(p, r));
-  }
-  if (tid == 0) scan.req = -1;
-  const int64_t upto = pair_scan(mine, scan.warp_sum);
-  if (tid == kPairThreads - 1) scan.total = upto;
-  __syncthreads();
-  const int64_t total = scan.total;
-  const int64_t range = max((total + pairs - 1) / pairs, static_cast<int64_t>(kMinRange));
-  const int64_t v0 = pair * range, v1 = v0 + range;
-  if (p.n_req <= kPairThreads) {
-    if (upto - mine <= v0 && v0 < upto) {
-      scan.req = tid;
-      scan.start = upto - mine;
-    }
+  if (p.n_req > 32) {
+    int64_t mine = 0;
+    for (int64_t b = tid; b < p.n_req; b += kPairThreads) mine += axis_of(p, request(p, b));
+    if (tid == 0) scan.req = -1;
+    const int64_t upto = pair_scan(mine, scan.warp_sum);
+    if (tid == kPairThreads - 1) scan.total = scan.run = upto;
     __syncthreads();
-  } else if (v0 < total) {
-    int64_t run = 0;
-    for (int64_t b0 = 0; b0 < p.n_req && run <= v0; b0 += kPairThreads) {
-      int64_t cost = 0;
-      if (b0 + tid < p.n_req) {
-        const Request r = request(p, b0 + tid);
-        cost = p.groups * axis_of(p, r, token_tiles(p, r));
+    const int64_t v0 = pair * range_of(scan.total, pairs);
+    if (p.n_req <= kPairThreads) {
+      if (upto - mine <= v0 && v0 < upto) {
+        scan.req = tid;
+        scan.start = upto - mine;
       }
-      const int64_t end = run + pair_scan(cost, scan.warp_sum);
-      if (end - cost <= v0 && v0 < end) {
-        scan.req = b0 + tid;
-        scan.start = end - cost;
+      __syncthreads();
+    } else if (v0 < scan.total) {
+      int64_t run = 0;
+      for (int64_t b0 = 0; b0 < p.n_req && run <= v0; b0 += kPairThreads) {
+        const int64_t cost = b0 + tid < p.n_req ? axis_of(p, request(p, b0 + tid)) : 0;
+        const int64_t end = run + pair_scan(cost, scan.warp_sum);
+        if (end - cost <= v0 && v0 < end) {
+          scan.req = b0 + tid;
+          scan.start = end - cost;
+        }
+        if (tid == kPairThreads - 1) scan.run = end;
+        __syncthreads();
+        run = scan.run;
+        __syncthreads();
       }
-      if (tid == kPairThreads - 1) scan.total = end;
-      __syncthreads();
-      run = scan.total;
-      __syncthreads();
     }
   }
   __syncwarp();
   cluster_wait();     // and those of the other CTA
   tc_fence_after();
   const uint32_t tmem = c.tmem_slot;
-  const int64_t first_req = scan.req;
 
   if (warp >= 4 && warp < 8) {
     // ============================================================ softmax and rescaling
@@ -495,11 +499,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const int row4 = row - (lane & 3);
       __nv_bfloat16* out = p.out + (q_row + row4) * kDv + 256 * half + 8 * (lane & 3);
       float4* po = reinterpret_cast<float4*>(p.part_o) + (static_cast<int64_t>(part) * 128 + 64 * half) * p.row_cap + row;
-#pragma unroll 1
-      for (int i = 0; i < 8; ++i) {
-        uint32_t o[32];
-        tmem_ld32(lanes + 32 * i, o);
-        tmem_ld_wait();
+      auto put = [&](const uint32_t(&o)[32], int i) {   // columns 32 i .. 32 i + 31
         if (part < 0) {
           uint32_t v[4][4];
 #pragma unroll
@@ -519,11 +519,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                                                       __uint_as_float(o[4 * j + 2]), __uint_as_float(o[4 * j + 3]));
         }
         __syncwarp();
+      };
+#pragma unroll 1
+      for (int i = 0; i < 8; i += 2) {
+        uint32_t o0[32], o1[32];
+        tmem_ld32(lanes + 32 * i, o0);
+        tmem_ld32(lanes + 32 * i + 32, o1);
+        tmem_ld_wait();
+        if (i == 6) {   // O has been read: the next tile's first PV may overwrite it
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_pair(o_free);
+        }
+        put(o0, i);
+        put(o1, i + 1);
       }
-      // O has been read: the next tile's first PV may overwrite it
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_pair(o_free);
     }
   } else {
     if (warp == 0) {
@@ -541,23 +551,61 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     };
     int4 join = make_int4(0, 0, -1, 0);
     int64_t join_end = 0;
+    const bool few = p.n_req <= 32;
+    Request mine{};                              // few requests: lane i has request i
+    int64_t total, start, first_req;             // start: the request's position on the axis
+    int64_t range, v0;
+    if (few) {
+      int64_t cost = 0;
+      if (lane < p.n_req) {
+        mine = request(p, lane);
+        cost = axis_of(p, mine);
+      }
+      int64_t end = cost;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(0xffffffffu, end, o);
+        if (lane >= o) end += u;
+      }
+      total = __shfl_sync(0xffffffffu, end, 31);
+      range = range_of(total, pairs);
+      v0 = pair * range;
+      const uint32_t hit = __ballot_sync(0xffffffffu, end - cost <= v0 && v0 < end);
+      first_req = __ffs(hit) - 1;                // -1: the range lies behind the axis' end
+      start = __shfl_sync(0xffffffffu, end - cost, hit ? __ffs(hit) - 1 : 0);
+    } else {
+      total = scan.total;
+      range = range_of(total, pairs);
+      v0 = pair * range;
+      first_req = scan.req;
+      start = scan.start;
+    }
+    const int64_t v1 = v0 + range;
     bool more = v0 < total && first_req >= 0;
-    int64_t start = more ? scan.start : 0;       // the request's position on the axis
     for (int64_t req = first_req; more && req < p.n_req && !stop; ++req) {
-      const Request r = request(p, req);
+      Request r;
+      if (few) {
+        const int from = static_cast<int>(req);
+        r.q0 = __shfl_sync(0xffffffffu, mine.q0, from);
+        r.n_q = __shfl_sync(0xffffffffu, mine.n_q, from);
+        r.n_k = __shfl_sync(0xffffffffu, mine.n_k, from);
+        r.keys = __shfl_sync(0xffffffffu, mine.keys, from);
+      } else {
+        r = request(p, req);
+      }
       const int64_t n_tiles = token_tiles(p, r);
       const int64_t before = r.n_k - r.n_q;      // position of the request's first new token
-      int64_t k = 0;
+      int64_t k = 0, s = start;                  // token tile, its position on the axis
       if (start < v0) {   // the range starts inside this request: last token tile that begins at or before v0
         int64_t lo = 0, hi = n_tiles;
         while (hi - lo > 1) {
           const int64_t mid = (lo + hi) >> 1;
-          if (p.groups * axis_of(p, r, mid) <= v0 - start) lo = mid;
+          if (axis_of(p, r, mid, n_tiles) <= v0 - start) lo = mid;
           else hi = mid;
         }
         k = lo;
+        s = start + axis_of(p, r, k, n_tiles);
       }
-      int64_t s = start + p.groups * axis_of(p, r, k);   // the tile's position on the axis
       for (; k < n_tiles && more && !stop; ++k) {
         const int64_t tok = k * p.tokens_per_tile, last = min(r.n_q, tok + p.tokens_per_tile);
         const int64_t size = kTileCost + (p.causal ? max(before, static_cast<int64_t>(0)) + last : r.n_k);
@@ -615,7 +663,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           }
         }
       }
-      start += p.groups * axis_of(p, r, n_tiles);
+      start = s;
     }
     if (join.z == 0) join.z = static_cast<int>(join_end / range);
     acquire();
@@ -763,23 +811,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                          (!first || ks > 0) ? 1u : 0u);
         umma_commit_pair(smem_u32(&c.pv_done[g]));
       }
+      // the only arrivals of the other CTA that nothing else waits for: it may not outlive them
+      if (tiles > 0) wait_on_pair(&c.o_free, (tiles - 1) & 1, abort);
     }
     __syncwarp();
   }
   }
 
-  // ---- every copy and product has been waited for (each tile's epilogue follows its last PV) unless a
-  // wait gave up; then what is still in flight gets time to land before the CTAs leave
+  // ---- Every copy and product has been waited for (each tile's epilogue follows its last PV) unless a wait
+  // gave up, in either CTA; then what is still in flight gets time to land before the CTAs leave.
+  __syncwarp();
+  if (*abort && lane == 0) store_pair(map_to_rank(smem_u32(&c.abort_flag), 1 - rank), 1);
   __syncwarp();
   tc_fence_before();
-  cluster_sync();
+  if (*abort) cluster_arrive();
+  else cluster_arrive_relaxed();   // nothing to publish: the kernel's end makes its results visible
+  cluster_wait();
   if (*abort) {
     const uint64_t t0 = globaltimer_ns();
     while (globaltimer_ns() - t0 < 5000000ull) {
     }
+    __syncwarp();
   }
-  __syncwarp();
-  cluster_sync();
   if (warp == 3) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, kTmemCols);
