@@ -843,62 +843,79 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 // A tile cut over pairs w .. w1 left its parts in slots 2w + 1, 2(w+1), .., 2 w1.  With M = max m_i:
 //   l = sum 2^(m_i - M) l_i,   O = sum 2^(m_i - M) O_i / (l + [sink] 2^(sink log2 e - M)).
 // A CTA takes 32 rows and 128 columns, a lane a row: the parts are read as they were written, 16 bytes of 32
-// rows at a time, and the output leaves through shared memory in whole row pieces.
+// rows at a time, with the loads of four parts in flight (their latency is what the kernel's time is), and
+// the output leaves through shared memory in whole row pieces.
 constexpr int kJoinRows = 32;
-constexpr int kJoinThreads = 256;
+constexpr int kJoinWarps = 8;                 // two column quads each
+constexpr int kJoinParts = 3;
 
-__global__ void __launch_bounds__(kJoinThreads) chunk_join_kernel(const ChunkParams p) {
-  __shared__ __align__(16) uint2 tile[kJoinRows][33];   // four columns each; padded against bank conflicts
+__global__ void __launch_bounds__(32 * kJoinWarps) chunk_join_kernel(const ChunkParams p) {
+  __shared__ __align__(16) uint2 tile[kJoinRows][17];   // four columns each; padded against bank conflicts
   const int w = blockIdx.x;
   cudaGridDependencySynchronize();
   const int4 join = p.joins[w];
   const int row0 = blockIdx.y * kJoinRows;
   if (join.z < 0 || row0 >= join.y) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = row0 + lane;
-  const int col4 = 32 * blockIdx.z + 4 * warp;          // four column quads of this warp
-  const bool live = row < join.y;
-  auto slot = [&](int i) { return i == w ? 2 * w + 1 : 2 * i; };
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row = min(row0 + lane, join.y - 1);         // lanes behind the last row repeat it
+  const int64_t r = static_cast<int64_t>(join.x) + row;
+  const float sink2 = p.attn_sink ? __ldg(p.attn_sink + r % p.h_q) * kLog2e : -INFINITY;
   const float* stats = p.part_stats + row;
+  const float4* part = reinterpret_cast<const float4*>(p.part_o) + (16 * blockIdx.z + 2 * warp) * p.row_cap + row;
   float M = -INFINITY, top = -INFINITY, l = 0.f;
-  float4 acc[4] = {};
-  if (live) {
-#pragma unroll 4
-    for (int i = w; i <= join.z; ++i) M = fmaxf(M, stats[slot(i) * 3 * 128]);
-    const float base = M > -INFINITY ? M : 0.f;
-#pragma unroll 2
-    for (int i = w; i <= join.z; ++i) {
-      const float* st = stats + slot(i) * 3 * 128;
-      const float4* o = reinterpret_cast<const float4*>(p.part_o) + (static_cast<int64_t>(slot(i)) * 128 + col4) * p.row_cap + row;
-      const float a = exp2f(st[0] - base);
-      l = fmaf(a, st[128], l);
-      top = fmaxf(top, st[256]);
+  float4 acc[2] = {};
+  for (int i0 = w; i0 <= join.z; i0 += kJoinParts) {
+    float m[kJoinParts], li[kJoinParts], ti[kJoinParts];
+    float4 o[kJoinParts][2];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const float4 v = o[x * p.row_cap];
-        acc[x].x = fmaf(a, v.x, acc[x].x);
-        acc[x].y = fmaf(a, v.y, acc[x].y);
-        acc[x].z = fmaf(a, v.z, acc[x].z);
-        acc[x].w = fmaf(a, v.w, acc[x].w);
+    for (int u = 0; u < kJoinParts; ++u) {
+      const int i = min(i0 + u, join.z), slot = i == w ? 2 * w + 1 : 2 * i;
+      const float* st = stats + slot * 3 * 128;
+      m[u] = st[0];
+      li[u] = st[128];
+      ti[u] = st[256];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) o[u][x] = part[(static_cast<int64_t>(slot) * 128 + x) * p.row_cap];
+    }
+    float now = M;
+#pragma unroll
+    for (int u = 0; u < kJoinParts; ++u)
+      if (i0 + u <= join.z) now = fmaxf(now, m[u]);
+    const float base = now > -INFINITY ? now : 0.f, keep = exp2f(M - base);
+    M = now;
+    l *= keep;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) acc[x] = make_float4(acc[x].x * keep, acc[x].y * keep, acc[x].z * keep, acc[x].w * keep);
+#pragma unroll
+    for (int u = 0; u < kJoinParts; ++u) {
+      if (i0 + u > join.z) break;
+      const float a = exp2f(m[u] - base);
+      l = fmaf(a, li[u], l);
+      top = fmaxf(top, ti[u]);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        acc[x].x = fmaf(a, o[u][x].x, acc[x].x);
+        acc[x].y = fmaf(a, o[u][x].y, acc[x].y);
+        acc[x].z = fmaf(a, o[u][x].z, acc[x].z);
+        acc[x].w = fmaf(a, o[u][x].w, acc[x].w);
       }
     }
   }
   const bool empty = !(l > 0.f);
-  const int64_t r = static_cast<int64_t>(join.x) + row;
-  float den = l;
-  if (p.attn_sink && live && !empty) den += exp2f(fmaf(__ldg(p.attn_sink + r % p.h_q), kLog2e, -M));
+  const float den = p.attn_sink && !empty ? l + exp2f(sink2 - M) : l;
   const float inv = empty ? 0.f : 1.f / den;
 #pragma unroll
-  for (int x = 0; x < 4; ++x)
-    tile[lane][4 * warp + x] = empty ? make_uint2(0u, 0u)
+  for (int x = 0; x < 2; ++x)
+    tile[lane][2 * warp + x] = empty ? make_uint2(0u, 0u)
                                      : make_uint2(pack_bf16x2(acc[x].x * inv, acc[x].y * inv),
                                                   pack_bf16x2(acc[x].z * inv, acc[x].w * inv));
-  if (live && warp == 0 && blockIdx.z == 0) {
+  if (row0 + lane < join.y && warp == 0 && blockIdx.z == 0) {
     p.lse[r] = empty ? INFINITY : (M + log2f(l)) * kLn2;
     p.max_logits[r] = empty ? -INFINITY : top;
   }
   __syncthreads();
-  for (int k = warp; k < kJoinRows && row0 + k < join.y; k += kJoinThreads / 32)
-    reinterpret_cast<uint2*>(p.out + (static_cast<int64_t>(join.x) + row0 + k) * kDv + 128 * blockIdx.z)[lane] = tile[k][lane];
+  for (int k = warp; k < kJoinRows && row0 + k < join.y; k += kJoinWarps)
+    if (lane < 16) reinterpret_cast<uint2*>(p.out + (static_cast<int64_t>(join.x) + row0 + k) * kDv + 64 * blockIdx.z)[lane] = tile[k][lane];
 }
 
 // ------------------------------------------------------------------------ host side
@@ -980,8 +997,8 @@ smla_status launch(const CUtensorMap& qm, const CUtensorMap& hm, const CUtensorM
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(pairs, (p.row_cap + kJoinRows - 1) / kJoinRows, kDv / 128);
-  cfg.blockDim = dim3(kJoinThreads);
+  cfg.gridDim = dim3(pairs, (p.row_cap + kJoinRows - 1) / kJoinRows, kDv / 64);
+  cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = stream;
   cfg.attrs = &early;
   cfg.numAttrs = 1;
