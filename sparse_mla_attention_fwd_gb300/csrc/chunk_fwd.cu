@@ -66,8 +66,8 @@ constexpr int kGens = 4;                  // key buffers, S buffers
 constexpr int kRing = 4;                  // block descriptors ahead
 constexpr int kPairThreads = 416;
 constexpr int kMaxPairs = 80;             // ranges the axis is cut into, at most
-constexpr int kTileCost = 256;            // start and end of a tile, in keys
-constexpr int kMinRange = 128;            // shortest range, in keys (at least kKeys)
+constexpr int kTileCost = 192;            // start and end of a tile, in keys
+constexpr int kMinRange = 256;            // shortest range, in keys (at least kKeys)
 constexpr uint32_t kHalfBytes = 16384;    // 32 keys x 256 columns
 constexpr uint32_t kPBytes = 8192;        // 64 rows x 64 keys
 constexpr uint32_t kTmemCols = 512, kTmemS = 256;
@@ -552,7 +552,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     int4 join = make_int4(0, 0, -1, 0);
     int64_t join_end = 0;
     const bool few = p.n_req <= 32;
-    Request mine{};                              // few requests: lane i has request i
+    Request mine{};                              // of request `window` + lane
+    int64_t window = 0;
     int64_t total, start, first_req;             // start: the request's position on the axis
     int64_t range, v0;
     if (few) {
@@ -582,17 +583,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
     const int64_t v1 = v0 + range;
     bool more = v0 < total && first_req >= 0;
-    for (int64_t req = first_req; more && req < p.n_req && !stop; ++req) {
-      Request r;
-      if (few) {
-        const int from = static_cast<int>(req);
-        r.q0 = __shfl_sync(0xffffffffu, mine.q0, from);
-        r.n_q = __shfl_sync(0xffffffffu, mine.n_q, from);
-        r.n_k = __shfl_sync(0xffffffffu, mine.n_k, from);
-        r.keys = __shfl_sync(0xffffffffu, mine.keys, from);
-      } else {
-        r = request(p, req);
+    if (!few) window = -32;                      // loaded below
+    for (int64_t req = first_req; more && req < p.n_req && start < total && !stop; ++req) {
+      if (req >= window + 32 || window < 0) {
+        window = req;
+        mine = Request{};
+        if (window + lane < p.n_req) mine = request(p, window + lane);
       }
+      // the next request with tokens
+      const uint32_t live = __ballot_sync(0xffffffffu, mine.n_q > 0) >> (req - window);
+      if (live == 0u) {
+        req = window + 31;
+        continue;
+      }
+      req += __ffs(live) - 1;
+      const int from = static_cast<int>(req - window);
+      Request r;
+      r.q0 = __shfl_sync(0xffffffffu, mine.q0, from);
+      r.n_q = __shfl_sync(0xffffffffu, mine.n_q, from);
+      r.n_k = __shfl_sync(0xffffffffu, mine.n_k, from);
+      r.keys = __shfl_sync(0xffffffffu, mine.keys, from);
       const int64_t n_tiles = token_tiles(p, r);
       const int64_t before = r.n_k - r.n_q;      // position of the request's first new token
       int64_t k = 0, s = start;                  // token tile, its position on the axis

@@ -519,3 +519,16 @@ def test_serving_steps_together():
                 assert float((out[t0:t1].float() - o2.float()).abs().max()) <= 4.2 * U16 * float(pool[table[b][table[b] >= 0].long()[:, None] * page].float().nan_to_num().abs().max().clamp(min=5.0))
         assert int(counts[0]) == sum(new) and int(counts[2]) == 0
         seqlens, start = seqlens_k, counts[1:2].clone()
+
+
+def test_chunk_batch_with_empty_slots():
+    """Many request slots, few of them with tokens: at the front, scattered, and at the end."""
+    for seed, live in ((0, range(5)), (1, range(3, 900, 97)), (2, [899]), (3, [])):
+        q_lens, k_lens = [0] * 900, [11] * 900
+        for i in live:
+            q_lens[i], k_lens[i] = 1 + i % 3, 50 + i
+        chunk_check(chunk_case(seed, q_lens, k_lens, 16, 512, page=16, tail=2))
+
+
+def test_chunk_of_1024_heads():
+    chunk_check(chunk_case(20, [2, 1], [140, 33], 1024, 512))
