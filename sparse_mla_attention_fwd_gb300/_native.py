@@ -35,6 +35,8 @@ class SmlaError(RuntimeError):
 def load_library(path: str | None = None):
     """Load (once) and return the ctypes handle of the CUDA library."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
