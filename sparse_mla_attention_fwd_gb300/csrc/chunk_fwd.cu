@@ -24,10 +24,10 @@
 // 0-255 (value columns 0-255 in lanes 0-63, 256-511 in lanes 64-127), S of block b in columns
 // 256 + 32 (b % 4) (keys 0-31 in lanes 0-63, 32-63 in lanes 64-127).
 //
-// Warps (288 threads): 0 scheduler, 1 K loads, 2 foreign-half and Q loads, 3 S issuer, 4-7 softmax
-// and epilogue (TMEM lane quadrants 0-3), 8 PV issuer; the issuers work in the pair's first CTA.
-// Four buffers of keys: S runs up to three blocks ahead of P V, so the second load of a block and the
-// softmax have one to two blocks' time.
+// Warps: 0 scheduler, 1 K loads, 2 foreign-half and Q loads, 3 S issuer, 4-7 softmax, 8-11 epilogue
+// (both on TMEM lane quadrants 0-3), 12 PV issuer; the issuers work in the pair's first CTA.  Four buffers of
+// keys: S runs up to three blocks ahead of P V, so the second load of a block and the softmax have one to
+// two blocks' time.
 //
 // Work split.  Tiles times key blocks are laid out on one axis, a tile's cost being its keys plus a
 // constant for its start and end, and the axis is cut into equal ranges, one per pair: a long
@@ -35,6 +35,15 @@
 // lengths with closed-form sums (no host step, no planning launch).  A tile that lies in one range is
 // finished there; parts of a cut tile go to the workspace (at most two per pair) and a second
 // kernel joins them.  Nothing depends on timing, so results are the same bits from call to call.
+//
+// What bounds it.  A block takes 1412 cycles of the tensor unit at full rate (36 products of N = 64, which the
+// operands' 3 KB at 128 bytes a cycle of shared memory hold at 25 cycles instead of 16, and 8 of N = 256 at 64),
+// about 1690 of shared memory (216 KB: operands, arriving keys, P), and 1400 of the L2's delivery (52 KB at the
+// 37 bytes a cycle and SM that loads of all SMs together reach).  It runs at about 1780: 4 x 512 tokens behind
+// 2048-8192 keys, 64 heads, 0.95 ms = 1450 TFLOP/s, tensor unit busy 64 % of the cycles, L2 at 9.5 TB/s; 2048
+// tokens over 8192 keys, 128 heads, 2.81 ms = 1456 TFLOP/s; 256 tokens of one request each over 1024-4096 keys,
+// 128 heads, 162 us = 5.1 TB/s.  Blocks of 128 keys (less operand traffic, two buffers instead of four) ran at the
+// same pace on chunks and 12 % slower on single tokens, where two buffers do not cover the latency of HBM.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -66,8 +75,12 @@ constexpr int kGens = 4;                  // key buffers, S buffers
 constexpr int kRing = 4;                  // block descriptors ahead
 constexpr int kPairThreads = 416;
 constexpr int kMaxPairs = 80;             // ranges the axis is cut into, at most
-constexpr int kTileCost = 192;            // start and end of a tile, in keys
-constexpr int kMinRange = 256;            // shortest range, in keys (at least kKeys)
+// Start and end of a tile, in keys (two blocks' time measured between tiles; 128 to 512 differ by 1 % on 256
+// requests), and the shortest range: many parts of a tile cost more to join than longer ones to walk (one
+// token over 1500 keys: 128 17.4 us, 256 15.8 us, 320 16.2 us).  kMinRange is at least kKeys, so that every
+// pair between a cut tile's ends has a part of it.
+constexpr int kTileCost = 192;
+constexpr int kMinRange = 256;
 constexpr uint32_t kHalfBytes = 16384;    // 32 keys x 256 columns
 constexpr uint32_t kPBytes = 8192;        // 64 rows x 64 keys
 constexpr uint32_t kTmemCols = 512, kTmemS = 256;
@@ -206,8 +219,7 @@ __device__ __forceinline__ void give_up(volatile int* abort) {
   atomicExch(&g_chunk_status, static_cast<int>(SMLA_ERR_DEVICE_TIMEOUT));
 }
 
-// A waiting thread sleeps on the barrier rather than polling it: the polls of a dozen warps take shared-memory
-// cycles from the tensor unit's operands.
+// The clock and the abort flag are looked at every 16 tries: with both in every try the kernel is 2 % slower.
 template <bool PAIR>
 __device__ __forceinline__ void wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort) {
   constexpr uint32_t kSleepNs = 100000;
@@ -215,10 +227,9 @@ __device__ __forceinline__ void wait_bounded(uint64_t* bar, uint32_t parity, vol
   auto done = [&] { return PAIR ? mbar_sleep_cluster(a, parity, kSleepNs) : mbar_sleep(a, parity, kSleepNs); };
   if (done()) return;
   const uint64_t t0 = globaltimer_ns();
-  uint32_t spins = 0;
-  while (!done()) {
-    if ((++spins & 15u) == 0u && (*abort || globaltimer_ns() - t0 > kWaitLimitNs)) return give_up(abort);
-  }
+  uint32_t tries = 0;
+  while (!done())
+    if ((++tries & 15u) == 0u && (*abort || globaltimer_ns() - t0 > kWaitLimitNs)) return give_up(abort);
 }
 __device__ __forceinline__ void wait_on(uint64_t* bar, uint32_t parity, volatile int* abort) {
   wait_bounded<false>(bar, parity, abort);
@@ -479,6 +490,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     named_bar_arrive(kTileBar + (tile & 1), 256);
   } else if (warp >= 8 && warp < 12) {
     // ============================================================ epilogue
+    // Warps of its own, so that the softmax of the next tile need not wait (9500 cycles between two tiles
+    // without, 3500 with them), asleep on a named barrier: waiting on an mbarrier, the four warps took so many issue
+    // slots from the softmax warps next to them that all calls ran 1.6 times as long.
     const int t = tid - 256, row = (t & 63) + 64 * static_cast<int>(rank), half = t >> 6;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(t & 96) << 16);
     const uint32_t o_free = map_to_rank(smem_u32(&c.o_free), 0);
@@ -535,8 +549,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         put(o1, i + 1);
       }
     }
-  } else {
-    if (warp == 0) {
+  } else if (warp == 0) {
     // ============================================================ scheduler
     int b = 0;
     bool stop = false;
@@ -685,8 +698,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   } else if (warp == 1 || warp == 2) {
     // ============================================================ key loads
     // Warp 1: all columns of the CTA's own 32 keys.  Warp 2: the CTA's value columns of the other CTA's 32
-    // keys, in place of the foreign half, and each tile's Q, as soon as S of the tile before is done.  One elected thread issues the loads: issued from several lanes,
-    // each costs the warp a turn.
+    // keys, in place of the foreign half, and each tile's Q, as soon as S of the tile before is done.  One
+    // elected thread issues the loads: issued from several lanes, each costs the warp a turn (a chunk of
+    // 2048 tokens took 2.95 ms instead of 2.85).
     const bool foreign = warp == 2;
     const uint32_t k_full = map_to_rank(smem_u32(&c.k_full[0]), 0), x_full = map_to_rank(smem_u32(&c.x_full[0]), 0);
     const uint32_t q_full = map_to_rank(smem_u32(&c.q_full), 0);
@@ -826,7 +840,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
     __syncwarp();
   }
-  }
 
   // ---- Every copy and product has been waited for (each tile's epilogue follows its last PV) unless a wait
   // gave up, in either CTA; then what is still in flight gets time to land before the CTAs leave.
@@ -852,9 +865,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 // ------------------------------------------------------------------------ joining cut tiles
 // A tile cut over pairs w .. w1 left its parts in slots 2w + 1, 2(w+1), .., 2 w1.  With M = max m_i:
 //   l = sum 2^(m_i - M) l_i,   O = sum 2^(m_i - M) O_i / (l + [sink] 2^(sink log2 e - M)).
-// A CTA takes 32 rows and 128 columns, a lane a row: the parts are read as they were written, 16 bytes of 32
-// rows at a time, with the loads of four parts in flight (their latency is what the kernel's time is), and
-// the output leaves through shared memory in whole row pieces.
+// A CTA takes 32 rows and 64 columns, a lane a row: the parts are read as they were written, 16 bytes of 32
+// rows at a time, with the loads of three parts in flight, and the output leaves through shared memory in
+// whole row pieces.  Latency bounds it: a round trip to parts that other SMs have just written takes 1.3 us.
+// The kernel adds 5 us to a call with twelve parts, 8 us to 256 requests (70 cut tiles, 36 MB of parts).
 constexpr int kJoinRows = 32;
 constexpr int kJoinWarps = 8;                 // two column quads each
 constexpr int kJoinParts = 3;

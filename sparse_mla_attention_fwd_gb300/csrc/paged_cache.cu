@@ -25,9 +25,10 @@ namespace {
 // CTAs in blocks of kPlanThreads, and a token (page) finds its request by a binary search in the
 // chunk's running sums.  Nothing that one CTA writes is read by another: a token in a page that
 // this launch hands out computes the page from the free list instead of reading the table.
-// The work is a few loads deep: latency bounds it, not bytes.
+// The work is a few loads deep: latency bounds it, not bytes, so a CTA takes about one token a thread (700 requests with
+// 41 k tokens: 8 us, with eight tokens a thread 14 us; 1024 threads and requests a chunk are no faster.  256
+// requests of one token: 4.3 us, 8 requests: 3.0 us).
 constexpr int kPlanThreads = 256;
-constexpr int kPlanTokensPerCta = 8 * kPlanThreads;
 constexpr int kPlanMaxCtas = 152;
 
 struct PlanParams {
@@ -85,9 +86,10 @@ __device__ __forceinline__ int owner_of(const T* end, int n, T x) {
   return lo;
 }
 
+// ceil(len / page_block), at most max_blocks; max_blocks * page_block fits 31 bits.
 __device__ __forceinline__ int32_t blocks_of(int64_t len, int32_t page_block, int32_t max_blocks) {
-  const int64_t n = (len + page_block - 1) / page_block;
-  return n < max_blocks ? static_cast<int32_t>(n) : max_blocks;
+  if (len >= static_cast<int64_t>(max_blocks) * page_block) return max_blocks;
+  return static_cast<int32_t>((static_cast<uint32_t>(len) + page_block - 1u) / static_cast<uint32_t>(page_block));
 }
 
 __global__ void __launch_bounds__(kPlanThreads) plan_pages_kernel(const PlanParams p) {
@@ -132,13 +134,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_pages_kernel(const PlanPara
         if (t < tok_run || t >= tok_next) continue;
         const int i = owner_of(c.tok_end, n, static_cast<int32_t>(t));
         const int64_t pos = static_cast<int64_t>(c.old_len[i]) + (t - c.tok_begin[i]);
-        const int64_t col = pos / p.page_block;
         int64_t slot = -1;
+        const int32_t col = pos <= INT32_MAX ? static_cast<int32_t>(pos) / p.page_block : p.max_blocks;
         if (col < p.max_blocks) {
           const int32_t page = col < c.first[i]
                                    ? p.block_table[(r0 + i) * p.max_blocks + col]
                                    : free_page((i > 0 ? c.page_end[i - 1] : page_run) + (col - c.first[i]));
-          slot = page < 0 ? -1 : static_cast<int64_t>(page) * p.page_block + (pos - col * p.page_block);
+          slot = page < 0 ? -1 : static_cast<int64_t>(page) * p.page_block + (pos - static_cast<int64_t>(col) * p.page_block);
           if (slot > INT32_MAX) slot = -1;
         }
         p.slots[t] = static_cast<int32_t>(slot);
@@ -179,7 +181,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_pages_kernel(const PlanPara
 //   (x_2i, x_2i+1) -> (x_2i cos_i - x_2i+1 sin_i, x_2i+1 cos_i + x_2i sin_i),
 // cos_i, sin_i from the row of the rope table at the token's position.  The same launch turns the
 // queries' rope columns of every head into q[..., 512:].  All arithmetic is in fp32 and each value
-// is rounded to bf16 once.  The bytes bound it: every input is read once and every output written once.
+// is rounded to bf16 once.  The bytes bound it: every input is read once and every output written once (8192
+// tokens, 16 heads: 54 MB in 9.9 us, 5.5 TB/s; 256 tokens, 128 heads: 9 MB in 2.6 us).
 // A warp takes one unit: the token's row (16 latent values a lane, the sum of squares over the
 // warp), or 16 heads of its queries (8 lanes a head, 16 bytes a lane, four loads in flight).
 constexpr int kAppendThreads = 256;
@@ -327,7 +330,7 @@ smla_status sparse_mla_plan_pages(const int32_t* seqlens, const int32_t* new_len
   }
   PlanParams p{seqlens, new_lens, block_table, free_pages, free_start, seqlens_k, cu_seqlens_q, slots, positions,
                counts, n_req, n_free, static_cast<int32_t>(n_tokens), max_blocks, page_block};
-  int64_t ctas = (n_tokens + kPlanTokensPerCta - 1) / kPlanTokensPerCta;
+  int64_t ctas = (n_tokens + kPlanThreads - 1) / kPlanThreads;
   ctas = ctas < 1 ? 1 : ctas > kPlanMaxCtas ? kPlanMaxCtas : ctas;
   plan_pages_kernel<<<static_cast<unsigned>(ctas), kPlanThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
   return cudaGetLastError() == cudaSuccess ? SMLA_OK : SMLA_ERR_LAUNCH;
