@@ -771,9 +771,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         if (elect_one()) {
           const uint32_t bar = k_full + 8 * g;
           if (rank == 0) mbar_arrive_expect_tx(smem_u32(&c.k_full[g]), 2 * L::kGenBytes);
+          if constexpr (kChunks > 8) load(d, 8, 1, gen + 2 * kHalfBytes, bar);
           load(d, 0, 4, gen, bar);
           load(d, 4, 4, gen + kHalfBytes, bar);
-          if constexpr (kChunks > 8) load(d, 8, 1, gen + 2 * kHalfBytes, bar);
         }
       }
       __syncwarp();
