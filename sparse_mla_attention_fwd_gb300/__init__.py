@@ -398,6 +398,16 @@ def _dense(t, name, dtype, dev=None):
     raise TypeError(f"{name} must be a torch.Tensor")
 
 
+def _int_output(t, name, n, dev):
+    """An int32 output [n]: the caller's, or a new one on the current device."""
+    if t is None:
+        return _empty_strided((n,), (1,), torch.int32)
+    _dense(t, name, torch.int32, dev)
+    if t.shape != (n,):
+        raise ValueError(f"{name} must be [{n}], got {list(t.shape)}")
+    return t
+
+
 def _strided(t, name, shape, dev):
     """The strides of a bf16 tensor of this shape whose last dimension is contiguous."""
     if isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.device == dev and t.shape == shape:
@@ -455,17 +465,9 @@ def sparse_mla_plan_pages(seqlens, new_lens, block_table, free_pages, n_tokens, 
         _dense(free_start, "free_start", i32, dev)
         if free_start.numel() != 1:
             raise ValueError("free_start must have one entry")
-    outs = []
-    for name, t, n in (("seqlens_k", seqlens_k, n_req), ("cu_seqlens_q", cu_seqlens_q, n_req + 1), ("slots", slots, n_tokens),
-                       ("positions", positions, n_tokens), ("counts", counts, 3)):
-        if t is None:
-            t = _empty_strided((n,), (1,), i32)
-        else:
-            _dense(t, name, i32, dev)
-            if t.shape != (n,):
-                raise ValueError(f"{name} must be [{n}], got {list(t.shape)}")
-        outs.append(t)
-    k, cu, sl, pos, cnt = outs
+    k, cu = _int_output(seqlens_k, "seqlens_k", n_req, dev), _int_output(cu_seqlens_q, "cu_seqlens_q", n_req + 1, dev)
+    sl, pos = _int_output(slots, "slots", n_tokens, dev), _int_output(positions, "positions", n_tokens, dev)
+    cnt = _int_output(counts, "counts", 3, dev)
     rc = lib.sparse_mla_plan_pages(
         seqlens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(), _ptr(free_start),
         k.data_ptr(), cu.data_ptr(), sl.data_ptr(), pos.data_ptr(), cnt.data_ptr(), n_req, free_pages.numel(), n_tokens,
