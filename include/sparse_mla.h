@@ -296,8 +296,9 @@ smla_status sparse_mla_plan_pages(const int32_t* seqlens, const int32_t* new_len
  *   q            [n, h_q, 576] bf16, 16-byte aligned; given exactly when q_pe is
  *   kv_pool      [pool_rows, d_qk] bf16, 16-byte aligned
  * Arithmetic is fp32, each value is rounded to bf16 once; without a norm weight (without rope) the
- * bits are copied.  Two tokens with one slot leave that row undefined.  kv_pool must not overlap
- * c_kv or k_pe (SMLA_ERR_BAD_SHAPE).  n == 0 is a no-op.
+ * bits are copied.  Two tokens with one slot leave that row undefined.  SMLA_ERR_BAD_SHAPE when
+ * kv_pool overlaps c_kv, k_pe, q_pe or q, or q overlaps c_kv, k_pe or, other than in place, q_pe.
+ * n == 0 is a no-op.
  */
 smla_status sparse_mla_append_kv(const void* c_kv, int64_t c_stride, const void* k_pe, int64_t k_stride,
                                  const int32_t* slots, const int32_t* positions, const float* rope, int64_t max_pos,

@@ -358,10 +358,19 @@ smla_status sparse_mla_append_kv(const void* c_kv, int64_t c_stride, const void*
       !aligned_to(rope, 16) || !aligned_to(q_pe, 16) || q_stride_t % 8 || q_stride_h % 8 || !aligned_to(q, 16) ||
       !aligned_to(kv_pool, 16) || !aligned_to(slots, 4) || !aligned_to(positions, 4))
     return SMLA_ERR_MISALIGNED;
-  // rows are written while others are still read
+  // rows are written while others are still read; the queries' columns may be turned where they are
   const size_t pool_bytes = static_cast<size_t>(pool_rows) * d_qk * 2;
-  if (overlap(kv_pool, pool_bytes, c_kv, (static_cast<size_t>(n - 1) * c_stride + kLatent) * 2) ||
-      overlap(kv_pool, pool_bytes, k_pe, (static_cast<size_t>(n - 1) * k_stride + kRope) * 2))
+  const size_t q_bytes = static_cast<size_t>(n) * (q ? h_q : 0) * d_qk * 2;
+  const size_t c_bytes = (static_cast<size_t>(n - 1) * c_stride + kLatent) * 2;
+  const size_t k_bytes = (static_cast<size_t>(n - 1) * k_stride + kRope) * 2;
+  const size_t q_pe_bytes =
+      q ? (static_cast<size_t>(n - 1) * q_stride_t + static_cast<size_t>(h_q - 1) * q_stride_h + kRope) * 2 : 0;
+  const bool in_place = q_pe == static_cast<const __nv_bfloat16*>(q) + kLatent && (n == 1 || q_stride_t == int64_t{h_q} * d_qk) &&
+                        (h_q == 1 || q_stride_h == d_qk);
+  if (overlap(kv_pool, pool_bytes, c_kv, c_bytes) || overlap(kv_pool, pool_bytes, k_pe, k_bytes) ||
+      overlap(kv_pool, pool_bytes, q_pe, q_pe_bytes) || overlap(kv_pool, pool_bytes, q, q_bytes) ||
+      overlap(q, q_bytes, c_kv, c_bytes) || overlap(q, q_bytes, k_pe, k_bytes) ||
+      (!in_place && overlap(q, q_bytes, q_pe, q_pe_bytes)))
     return SMLA_ERR_BAD_SHAPE;
   AppendParams p{};
   p.c_kv = static_cast<const __nv_bfloat16*>(c_kv);

@@ -72,6 +72,19 @@ def test_append_refusals(lib, kw, code):
     assert append(lib, **kw) == code
 
 
+Q, Q_PE = FAKE + 7 * STEP, FAKE + 6 * STEP
+
+
+@pytest.mark.parametrize("kw", [
+    dict(q_pe=Q), dict(q_pe=Q + 1024 - 16, qt=24 * 576, qh=576), dict(q_pe=Q + 1024, qt=24 * 576, qh=64),   # beside its place
+    dict(q_pe=Q + 1024, qt=64, qh=576), dict(q_pe=Q + 5 * 24 * 1152 - 16), dict(q_pe=Q, qt=0, qh=0),
+    dict(q=FAKE), dict(q=FAKE + STEP), dict(q=FAKE + 8 * STEP), dict(q=FAKE + 8 * STEP + 1152 * 127),
+    dict(q_pe=FAKE + 8 * STEP), dict(pool=Q_PE + 4096),
+])
+def test_append_refuses_overlapping_queries(lib, kw):
+    assert append(lib, **kw) == SHAPE
+
+
 def test_append_of_nothing(lib):
     assert append(lib, n=0, c=None, k=None, slots=None, positions=None) == 0
     assert append(lib, n=0, c=None, slots=None, **NO_ROPE) == 0
