@@ -37,13 +37,14 @@
 // kernel joins them.  Nothing depends on timing, so results are the same bits from call to call.
 //
 // What bounds it.  A block takes 1412 cycles of the tensor unit at full rate (36 products of N = 64, which the
-// operands' 3 KB at 128 bytes a cycle of shared memory hold at 25 cycles instead of 16, and 8 of N = 256 at 64),
-// about 1690 of shared memory (216 KB: operands, arriving keys, P), and 1400 of the L2's delivery (52 KB at the
-// 37 bytes a cycle and SM that loads of all SMs together reach).  It runs at about 1780: 4 x 512 tokens behind
-// 2048-8192 keys, 64 heads, 0.95 ms = 1450 TFLOP/s, tensor unit busy 64 % of the cycles, L2 at 9.5 TB/s; 2048
-// tokens over 8192 keys, 128 heads, 2.81 ms = 1456 TFLOP/s; 256 tokens of one request each over 1024-4096 keys,
-// 128 heads, 162 us = 5.1 TB/s.  Blocks of 128 keys (less operand traffic, two buffers instead of four) ran at the
-// same pace on chunks and 12 % slower on single tokens, where two buffers do not cover the latency of HBM.
+// operands' 3 KB at 128 bytes a cycle of shared memory hold at 25 cycles instead of 16, and 8 of N = 256 at 64).
+// Arriving keys (52 KB) and P want the same shared memory: 1690 cycles if nothing ran beside the products.  The
+// L2 delivers 52 KB in 1400 (37 bytes a cycle and SM when all SMs load).  4 x 512 tokens behind 2048-8192 keys, 64
+// heads: 1676 cycles a block over the whole launch, 0.94 ms = 1460 TFLOP/s, L2 to SM 9.7 TB/s; 2048 tokens over
+// 8192 keys, 128 heads: 2.74-2.79 ms = 1465-1490 TFLOP/s; 256 tokens of one request each over 1024-4096 keys, 128
+// heads: 164 us = 5.0 TB/s.  Blocks of 128 keys (less operand traffic, two buffers instead of four) ran at the
+// same pace on chunks and 12 % slower on single tokens.  Requesting keys two to eight blocks ahead into L2
+// made single tokens 6 to 20 % slower.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -3,6 +3,11 @@ serving step of the three together.
 
 References are plain loops (planning, whole numbers: equal) or 64-bit torch on the same inputs.
 Tolerances count roundings: u = 2^-8 for one rounding to bf16, 2^-24 for fp32."""
+import os
+import subprocess
+import sys
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -11,6 +16,7 @@ import sparse_mla_attention_fwd_gb300 as smla
 
 pytestmark = pytest.mark.gpu
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 U16, U32 = 2.0 ** -8, 2.0 ** -24
 
 
@@ -532,3 +538,95 @@ def test_chunk_batch_with_empty_slots():
 
 def test_chunk_of_1024_heads():
     chunk_check(chunk_case(20, [2, 1], [140, 33], 1024, 512))
+
+
+FIRST_CALLS_CAPTURED = """
+import sys
+sys.path.insert(0, sys.argv[1])
+import torch, sparse_mla_attention_fwd_gb300 as smla
+torch.manual_seed(0)
+pool = torch.randn(4 * 64, 1, 576, device="cuda").to(torch.bfloat16)
+q, x = (torch.randn(*s, device="cuda").to(torch.bfloat16) for s in ((3, 16, 576), (3, 576)))
+lens, new, free = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([100, 64], [2, 1], [3, 2]))
+table = torch.tensor([[0, 1, -1], [2, -1, -1]], dtype=torch.int32, device="cuda")
+torch.cuda.synchronize()
+def step():
+    k, cu, slots, pos, counts = smla.sparse_mla_plan_pages(lens, new, table, free, 3)
+    smla.sparse_mla_append_kv(x[:, :512], x[:, 512:], slots, pool)
+    return smla.sparse_mla_chunk_fwd_paged(q, pool, table, cu, k)
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    captured = step()
+graph.replay()
+torch.cuda.synchronize()
+captured = [t.clone() for t in captured]
+assert all(torch.equal(a, b) for a, b in zip(captured, step())) and smla.sparse_mla_device_status() == 0
+"""
+
+
+def test_first_calls_of_a_process_may_be_captured():
+    done = subprocess.run([sys.executable, "-c", FIRST_CALLS_CAPTURED, ROOT], capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]
+
+
+def test_a_whole_step_in_one_graph():
+    """Plan, append and attend captured once; replayed over steps whose lengths, free list position and
+    inputs change in place, against the same steps run call by call."""
+    torch.manual_seed(4)
+    n_req, heads, page, width, n, steps = 6, 16, 16, 12, 64, ([20, 0, 7, 1, 16, 3], [1, 33, 1, 0, 1, 20], [1] * 6, [0] * 6)
+    free, rope = i32(np.random.default_rng(2).permutation(60)), rope_table(256)
+
+    def fresh():
+        return dict(lens=i32([0] * n_req), new=i32([0] * n_req), start=i32([0]), table=i32(np.full((n_req, width), -1)),
+                    pool=torch.zeros(60 * page, 1, 576, dtype=torch.bfloat16, device="cuda"),
+                    x=torch.zeros(n, 576, dtype=torch.bfloat16, device="cuda"),
+                    q=torch.zeros(n, heads, 576, dtype=torch.bfloat16, device="cuda"))
+
+    def step(s):
+        k, cu, slots, pos, counts = smla.sparse_mla_plan_pages(s["lens"], s["new"], s["table"], free, n, page_block=page,
+                                                               free_start=s["start"])
+        smla.sparse_mla_append_kv(s["x"][:, :512], s["x"][:, 512:], slots, s["pool"], positions=pos, rope=rope,
+                                  q_pe=s["q"][..., 512:], q=s["q"])
+        got = smla.sparse_mla_chunk_fwd_paged(s["q"], s["pool"], s["table"], cu, k, page_block=page)
+        s["lens"].copy_(k)
+        s["start"].copy_(counts[1:2])
+        return (*got, slots, pos, counts)
+
+    a, b = fresh(), fresh()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step(b)
+    for new in steps:
+        x, q = torch.randn(n, 576, device="cuda"), torch.randn(n, heads, 576, device="cuda")
+        for s in (a, b):
+            s["new"].copy_(i32(new))
+            s["x"].copy_(x)
+            s["q"].copy_(q)
+        want = step(a)
+        graph.replay()
+        used = sum(new)
+        assert all(torch.equal(u[:used], v[:used]) for u, v in zip(want[:3], captured[:3]))
+        assert all(torch.equal(u, v) for u, v in zip(want[3:], captured[3:]))
+        assert all(torch.equal(a[key], b[key]) for key in ("lens", "start", "table", "pool", "q"))
+    assert int(captured[5][2]) == 0
+
+
+def test_threads_call_at_once():
+    """Four threads, a stream each, over one cache."""
+    w = chunk_case(21, [1, 40, 3], [3000, 400, 901], 64)
+    want = smla.sparse_mla_chunk_fwd_paged(**w)
+    torch.cuda.synchronize()
+    same = []
+
+    def work():
+        s = torch.cuda.Stream()
+        got = [smla.sparse_mla_chunk_fwd_paged(**w, stream=s) for _ in range(20)]
+        s.synchronize()
+        same.append(all(torch.equal(x, y) for g in got for x, y in zip(want, g)))
+
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert same == [True] * 4
