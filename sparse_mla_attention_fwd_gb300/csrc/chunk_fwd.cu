@@ -453,7 +453,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         named_bar_sync(bar_id, 64);
         l += c.ex[(b + 1) & 1][t ^ 64];
         named_bar_sync(bar_id, 64);
-        const bool empty = !(l > 0.f);
+        // Without a key l is exactly 0; with one it is about 1 at least, the term of the row's largest score, or
+        // NaN.  fmaxf passes over NaN scores, so the maximum takes its NaN from the sum.
+        const bool empty = l == 0.f;
+        const float largest = empty ? -INFINITY : l == l ? top * p.sm_scale : l;
         const bool live = row < n_rows;
         float inv = 1.f;
         if (part < 0) {
@@ -463,13 +466,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           inv = empty ? 0.f : 1.f / den;
           if (live && half == 0) {
             p.lse[r] = empty ? INFINITY : (m + log2f(l)) * kLn2;
-            p.max_logits[r] = empty ? -INFINITY : top * p.sm_scale;
+            p.max_logits[r] = largest;
           }
         } else if (live && half == 0) {
           float* st = p.part_stats + part * 3 * 128 + row;
           st[0] = empty ? -INFINITY : m;
-          st[128] = empty ? 0.f : l;
-          st[256] = empty ? -INFINITY : top * p.sm_scale;
+          st[128] = l;
+          st[256] = largest;
         }
         // The epilogue warps take it from here.  Two slots are enough: this group's next tile but one comes
         // behind PV of its next tile, which waits until they have read O of this one.
@@ -926,7 +929,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) chunk_join_kernel(const Chunk
       }
     }
   }
-  const bool empty = !(l > 0.f);
+  const bool empty = l == 0.f;   // a part's NaN reaches the sum of all parts
   const float den = p.attn_sink && !empty ? l + exp2f(sink2 - M) : l;
   const float inv = empty ? 0.f : 1.f / den;
 #pragma unroll
@@ -936,7 +939,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) chunk_join_kernel(const Chunk
                                                   pack_bf16x2(acc[x].z * inv, acc[x].w * inv));
   if (row0 + lane < join.y && warp == 0 && blockIdx.z == 0) {
     p.lse[r] = empty ? INFINITY : (M + log2f(l)) * kLn2;
-    p.max_logits[r] = empty ? -INFINITY : top;
+    p.max_logits[r] = l == l ? top : l;   // -inf for an empty row
   }
   __syncthreads();
   for (int k = warp; k < kJoinRows && row0 + k < join.y; k += kJoinWarps)

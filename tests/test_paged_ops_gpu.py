@@ -630,3 +630,40 @@ def test_threads_call_at_once():
     for t in threads:
         t.join()
     assert same == [True] * 4
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("q_lens,k_lens,heads,d_qk", [([3], [70], 4, 576), ([1], [9000], 4, 576), ([40, 1], [700, 5000], 128, 512),
+                                                      ([2, 3], [900, 70], 200, 576)])
+def test_chunk_nan_queries_stay_visible(bad, q_lens, k_lens, heads, d_qk):
+    """A broken query gives NaN, not the values of a row that sees no key; every other row keeps its bits.  Whole tiles and
+    cut ones.  (An infinite column gives scores of both infinities, whose sum is NaN.)"""
+    w = chunk_case(heads, q_lens, k_lens, heads, d_qk)
+    sink = torch.randn(heads, device="cuda")
+    want = smla.sparse_mla_chunk_fwd_paged(**w, attn_sink=sink)
+    broken = torch.zeros(w["q"].shape[:2], dtype=torch.bool, device="cuda")
+    broken[0, 1] = broken[-1, heads - 1] = True
+    w["q"][..., 5] = torch.where(broken, bad, w["q"][..., 5])
+    got = smla.sparse_mla_chunk_fwd_paged(**w, attn_sink=sink)
+    for g, x in zip(got, want):
+        assert bool(g[broken].isnan().all())
+        assert torch.equal(g[~broken], x[~broken])
+
+
+def test_chunk_nan_keys_reach_the_tokens_that_see_them():
+    for n_k in (100, 9000):
+        w = chunk_case(22, [4, 2], [n_k, 90], 16)
+        at = n_k - 3                                   # the second token's own position
+        w["kv_pool"][w["block_table"][0, at // 64].long() * 64 + at % 64, 0, 7] = float("nan")
+        out, lse, top = smla.sparse_mla_chunk_fwd_paged(**w)
+        assert all(bool(x[1:4].isnan().all()) for x in (lse, top)) and bool(out[1:4].isnan().any(-1).all())
+        assert all(bool(torch.isfinite(x[4:].float()).all()) for x in (out, lse, top))
+
+
+def test_chunk_nan_does_not_hide_empty_rows():
+    w = chunk_case(23, [5, 3], [2, 0], 16)             # the first three tokens, and all of the second request, see no key
+    w["q"][:] = float("nan")
+    out, lse, top = smla.sparse_mla_chunk_fwd_paged(**w)
+    for rows in (slice(0, 3), slice(5, 8)):
+        assert bool((out[rows] == 0).all()) and bool((lse[rows] == float("inf")).all()) and bool((top[rows] == float("-inf")).all())
+    assert all(bool(x[3:5].isnan().all()) for x in (out, lse, top))
