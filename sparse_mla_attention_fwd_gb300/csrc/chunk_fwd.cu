@@ -87,7 +87,14 @@ constexpr uint32_t kPBytes = 8192;        // 64 rows x 64 keys
 constexpr uint32_t kTmemCols = 512, kTmemS = 256;
 
 enum : uint32_t { kFirst = 1u, kLast = 2u, kEnd = 4u };
-constexpr uint32_t kTileBar = 3;          // named barriers 1, 2: softmax warps that share rows; 3, 4: a tile is done
+// Named barriers 1, 2: softmax warps that share rows; kTileBar and on, in turn: a tile is done; kAgreeBar: all
+// softmax warps hand over a tile, or leave.  A wait on a named barrier has no time limit, so every one of these has to
+// complete whatever wait gave up, and when.  The softmax warps leave together (agreed on once a tile), so that all of them
+// have arrived for the same tiles.  The end's arrival then needs the epilogue past the barrier of the turn before, kTileBars
+// tiles back: with three it is, since the last tile handed over waited for PV of the one before, and that for the epilogue
+// of the one before it.
+constexpr uint32_t kTileBars = 3;
+constexpr uint32_t kTileBar = 3, kAgreeBar = kTileBar + kTileBars;
 
 __device__ int g_chunk_status = 0;        // SMLA_ERR_DEVICE_TIMEOUT once any wait gave up
 
@@ -168,7 +175,7 @@ struct Control {
   float inv[2][64];      // a finished tile's factor of each row, 0 for an empty row; by tile parity
   struct {
     int32_t q_row, n_rows, part, last;   // last: the tile's last block, or -1 behind the last tile
-  } done[2];
+  } done[kTileBars];
   uint64_t ring_full[kRing], ring_empty[kRing];
   uint64_t k_full[kGens], x_full[kGens];      // both CTAs' keys / foreign halves have landed (first CTA)
   uint64_t s_full[kGens], pv_done[kGens];     // S computed / PV done (both CTAs)
@@ -357,10 +364,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     uint8_t* p_row = s_p + (t & 63) * 128;
     const int sw = t & 7;
     float m = -INFINITY, top = -INFINITY, l = 0.f;   // exponent offset (log2 units), max of q.k, sum
-    int b = 0, tile = 0;
+    int b = 0;
+    uint32_t tile = 0;
     int limit = 0;                                   // first key position this row does not see
-    // The two warps that share rows meet at one barrier in every round, the last one included, and leave
-    // together, also when a wait gave up.
+    // The two warps that share rows meet at one barrier in every round, the last one included; all four meet at
+    // a tile's end, or else behind the loop.  So all leave in the same tile, also when a wait gave up.
+    bool agreed = false;
     for (;; ++b) {
       const BlockDesc& d = c.ring[b % kRing];
       const int g = b % kGens;
@@ -448,11 +457,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       if (lane == 0) mbar_arrive_pair(p_full);
 
       if (flags & kLast) {
-        // l of both key halves; the barrier behind it keeps the next block's maxima off these slots
+        // l of both key halves; the second barrier keeps the next block's maxima off these slots
         c.ex[(b + 1) & 1][t] = l;
         named_bar_sync(bar_id, 64);
         l += c.ex[(b + 1) & 1][t ^ 64];
-        named_bar_sync(bar_id, 64);
+        if (named_bar_or(kAgreeBar, 128, *abort != 0)) {
+          agreed = true;
+          break;
+        }
         // Without a key l is exactly 0; with one it is about 1 at least, the term of the row's largest score, or
         // NaN.  fmaxf passes over NaN scores, so the maximum takes its NaN from the sum.
         const bool empty = l == 0.f;
@@ -474,24 +486,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           st[128] = l;
           st[256] = largest;
         }
-        // The epilogue warps take it from here.  Two slots are enough: this group's next tile but one comes
-        // behind PV of its next tile, which waits until they have read O of this one.
+        // The epilogue warps take it from here.  Two slots of factors are enough: this group's next tile but one
+        // comes behind PV of its next tile, which waits until they have read O of this one.
         if (half == 0) c.inv[tile & 1][t] = inv;
         if (t == 0) {
-          c.done[tile & 1].q_row = static_cast<int32_t>(q_row);
-          c.done[tile & 1].n_rows = n_rows;
-          c.done[tile & 1].part = part;
-          c.done[tile & 1].last = b;
+          auto& done = c.done[tile % kTileBars];
+          done.q_row = static_cast<int32_t>(q_row);
+          done.n_rows = n_rows;
+          done.part = part;
+          done.last = b;
         }
-        named_bar_arrive(kTileBar + (tile & 1), 256);
+        named_bar_arrive(kTileBar + tile % kTileBars, 256);
         ++tile;
       }
     }
-    // PV of the last tile has waited for the epilogue of the one before, whose slot the end takes
+    if (!agreed) named_bar_or(kAgreeBar, 128, true);
     if (b > 0) wait_on(&c.pv_done[(b - 1) % kGens], ((b - 1) / kGens) & 1, abort);
-    if (t == 0) c.done[tile & 1].last = -1;
+    if (t == 0) c.done[tile % kTileBars].last = -1;
     __syncwarp();
-    named_bar_arrive(kTileBar + (tile & 1), 256);
+    named_bar_arrive(kTileBar + tile % kTileBars, 256);
   } else if (warp >= 8 && warp < 12) {
     // ============================================================ epilogue
     // Warps of its own, so that the softmax of the next tile need not wait (9500 cycles between two tiles
@@ -500,9 +513,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const int t = tid - 256, row = (t & 63) + 64 * static_cast<int>(rank), half = t >> 6;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(t & 96) << 16);
     const uint32_t o_free = map_to_rank(smem_u32(&c.o_free), 0);
-    for (int tile = 0;; ++tile) {
-      const auto& d = c.done[tile & 1];
-      named_bar_sync(kTileBar + (tile & 1), 256);   // the softmax warps arrive for each tile and for the end
+    for (uint32_t tile = 0;; ++tile) {
+      const auto& d = c.done[tile % kTileBars];
+      named_bar_sync(kTileBar + tile % kTileBars, 256);   // the softmax warps arrive for each tile and for the end
       const int last = d.last, n_rows = d.n_rows, part = d.part;
       if (last < 0) break;
       const int64_t q_row = d.q_row;
