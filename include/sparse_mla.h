@@ -288,8 +288,12 @@ smla_status sparse_mla_plan_pages(const int32_t* seqlens, const int32_t* new_len
  *   slots        [n] int32 pool rows; a negative one, or one >= pool_rows, is not written
  *   positions    [n] int32 rows of the rope table (with rope only)
  *   rope         [max_pos, 64] fp32, 16-byte aligned: 32 cosines, then 32 sines of a position; NULL
- *                for none.  A token whose position lies outside [0, max_pos) is padding: neither
- *                its cache row nor its q columns are written.
+ *                for none.  A token whose position lies outside [0, max_pos) is not written, neither
+ *                its cache row nor its q columns: negative positions are padding, those at or past
+ *                max_pos an error of the caller's, which sparse_mla_append_kv_counted reports.  The
+ *                planner gives a token a slot wherever the block table has a page for its position, and
+ *                the attention reads that row; with max_pos >= max_blocks * page_block every such row is
+ *                written.
  *   norm_weight  [512] bf16, 16-byte aligned, or NULL; eps finite and >= 0
  *   q_pe         [n, h_q, 64] bf16, strides q_stride_t and q_stride_h elements (multiples of 8),
  *                16-byte aligned, or NULL; needs rope.  It may be q[..., 512:] itself.
@@ -305,6 +309,18 @@ smla_status sparse_mla_append_kv(const void* c_kv, int64_t c_stride, const void*
                                  const void* norm_weight, float eps, const void* q_pe, int64_t q_stride_t,
                                  int64_t q_stride_h, void* q, int h_q, void* kv_pool, int64_t pool_rows, int d_qk,
                                  int64_t n, smla_stream_t stream);
+
+/*
+ * The same, and adds the number of tokens whose position is at or past max_pos to past_rope[0] (device
+ * memory, int32, 4-byte aligned, outside kv_pool, q, slots and positions; zeroed by the caller when the
+ * count is to start).  After such a token its request's keys are incomplete, and its q columns were not turned.
+ */
+smla_status sparse_mla_append_kv_counted(const void* c_kv, int64_t c_stride, const void* k_pe, int64_t k_stride,
+                                         const int32_t* slots, const int32_t* positions, const float* rope,
+                                         int64_t max_pos, const void* norm_weight, float eps, const void* q_pe,
+                                         int64_t q_stride_t, int64_t q_stride_h, void* q, int h_q, void* kv_pool,
+                                         int64_t pool_rows, int d_qk, int64_t n, int32_t* past_rope,
+                                         smla_stream_t stream);
 
 /*
  * Dense attention of a chunk of new tokens over a paged latent cache: the operation of

@@ -478,13 +478,16 @@ def sparse_mla_plan_pages(seqlens, new_lens, block_table, free_pages, n_tokens, 
 
 
 def sparse_mla_append_kv(c_kv, k_pe, slots, kv_pool, norm_weight=None, eps=1e-6, positions=None, rope=None, q_pe=None,
-                         q=None, stream=None):
+                         q=None, stream=None, past_rope=None):
     """Writes the rows of n new tokens into the paged cache: the latent part c_kv [n, 512] bf16
     (RMS-normalised with norm_weight [512] bf16 and eps when given) and, for d_qk 576, the rotary
     part k_pe [n, 64] bf16 (turned pair by pair when rope is given), to row slots[t] (int32; a
     token whose slot lies outside the pool is not written) of kv_pool [rows, 1, d_qk] bf16.  rope
-    [max_pos, 64] fp32 holds 32 cosines and 32 sines per position, positions [n] int32 the tokens'
-    (outside the table: padding, nothing is written).  With q_pe [n, h, 64] bf16, q[..., 512:] of q
+    [max_pos, 64] fp32 holds 32 cosines and 32 sines per position, positions [n] int32 the tokens'.
+    Outside the table nothing is written: negative positions are padding; one at or past max_pos
+    leaves its request without that row, and past_rope [1] int32, when given, is increased by the
+    number of such tokens (a table of max_blocks * page_block positions covers every row that the
+    planner gives).  With q_pe [n, h, 64] bf16, q[..., 512:] of q
     [n, h, 576] gets the queries' columns turned by the same angles.  c_kv, k_pe and q_pe may be
     strided views (slices of a projection's output) with a contiguous last dimension.  Returns
     kv_pool."""
@@ -492,7 +495,8 @@ def sparse_mla_append_kv(c_kv, k_pe, slots, kv_pool, norm_weight=None, eps=1e-6,
     bf16 = torch.bfloat16
     dev = _dense(kv_pool, "kv_pool", bf16)
     if stream is not None or torch.cuda.current_device() != dev.index:
-        return _on_device(sparse_mla_append_kv, dev, stream, c_kv, k_pe, slots, kv_pool, norm_weight, eps, positions, rope, q_pe, q)
+        return _on_device(sparse_mla_append_kv, dev, stream, c_kv, k_pe, slots, kv_pool, norm_weight, eps, positions, rope, q_pe, q,
+                          past_rope=past_rope)
     _dense(slots, "slots", torch.int32, dev)
     pool_shape = kv_pool.shape
     n, d_qk, pool_rows = slots.numel(), pool_shape[-1] if len(pool_shape) > 1 else 0, pool_shape[0]
@@ -529,12 +533,18 @@ def sparse_mla_append_kv(c_kv, k_pe, slots, kv_pool, norm_weight=None, eps=1e-6,
             raise ValueError("q must be [n, h, 576]")
         h_q = q_shape[1]
         q_strides = _strided(q_pe, "q_pe", (n, h_q, 64), dev)
+    if past_rope is not None:
+        _dense(past_rope, "past_rope", torch.int32, dev)
+        if past_rope.numel() != 1:
+            raise ValueError("past_rope must have one entry")
     if n == 0:
         return kv_pool
-    rc = lib.sparse_mla_append_kv(
+    append, last = (lib.sparse_mla_append_kv, ()) if past_rope is None else \
+        (lib.sparse_mla_append_kv_counted, (past_rope.data_ptr(),))
+    rc = append(
         c_kv.data_ptr(), c_stride, _ptr(k_pe), k_stride, slots.data_ptr(), _ptr(positions), _ptr(rope), max_pos,
         _ptr(norm_weight), float(eps), _ptr(q_pe), q_strides[0], q_strides[1], _ptr(q), h_q, kv_pool.data_ptr(), pool_rows,
-        d_qk, n, _raw_stream(dev.index))
+        d_qk, n, *last, _raw_stream(dev.index))
     if rc != 0:
         raise SmlaError(rc, "sparse_mla_append_kv")
     return kv_pool

@@ -19,7 +19,7 @@ EXPORTED = ("sparse_mla_fwd", "sparse_mla_fwd_paged", "sparse_mla_splitkv_worksp
             "sparse_mla_fwd_splitkv", "sparse_mla_fwd_paged_splitkv", "sparse_mla_fwd_paged_splitkv_static",
             "sparse_mla_fwd_host", "sparse_mla_selftest_wait_timeout", "sparse_mla_device_status",
             "sparse_mla_status_string", "sparse_mla_abi_version", "sparse_mla_bwd", "sparse_mla_plan_pages",
-            "sparse_mla_append_kv", "sparse_mla_chunk_workspace_size", "sparse_mla_chunk_fwd_paged",
+            "sparse_mla_append_kv", "sparse_mla_append_kv_counted", "sparse_mla_chunk_workspace_size", "sparse_mla_chunk_fwd_paged",
             "sparse_mla_chunk_device_status")
 
 _lock = threading.Lock()
@@ -82,6 +82,9 @@ def load_library(path: str | None = None):
         lib.sparse_mla_append_kv.restype = I32
         lib.sparse_mla_append_kv.argtypes = [P, I64, P, I64, P, P, P, I64, P, F32, P, I64, I64, P, I32, P, I64, I32,
                                              I64, P]
+        lib.sparse_mla_append_kv_counted.restype = I32
+        lib.sparse_mla_append_kv_counted.argtypes = [P, I64, P, I64, P, P, P, I64, P, F32, P, I64, I64, P, I32, P, I64,
+                                                     I32, I64, P, P]
         lib.sparse_mla_chunk_workspace_size.restype = SZ
         lib.sparse_mla_chunk_workspace_size.argtypes = [I64, I32]
         lib.sparse_mla_chunk_fwd_paged.restype = I32

@@ -200,6 +200,7 @@ struct AppendParams {
   const __nv_bfloat16* q_pe;        // or null
   __nv_bfloat16* q;
   __nv_bfloat16* pool;
+  int32_t* past_rope;               // or null
   int64_t c_stride, k_stride, q_stride_t, q_stride_h;   // elements
   int64_t max_pos, pool_rows, n;
   float eps;
@@ -288,10 +289,80 @@ __global__ void __launch_bounds__(kAppendThreads) append_kv_kernel(const AppendP
   int64_t pos = 0;
   if (p.rope) {
     pos = __ldg(p.positions + t);
-    if (pos < 0 || pos >= p.max_pos) return;   // a padding token: nothing is written for it
+    if (pos < 0 || pos >= p.max_pos) {   // padding, or behind the table: nothing is written for it
+      // a count, so the order of the additions does not matter
+      if (pos >= 0 && u == 0 && lane == 0 && p.past_rope) atomicAdd(p.past_rope, 1);
+      return;
+    }
   }
   if (u == 0) append_row(p, t, pos, lane);
   else turn_heads(p, t, pos, (u - 1) * kHeadsPerUnit, lane);
+}
+
+smla_status append_kv(const void* c_kv, int64_t c_stride, const void* k_pe, int64_t k_stride, const int32_t* slots,
+                      const int32_t* positions, const float* rope, int64_t max_pos, const void* norm_weight, float eps,
+                      const void* q_pe, int64_t q_stride_t, int64_t q_stride_h, void* q, int h_q, void* kv_pool,
+                      int64_t pool_rows, int d_qk, int64_t n, int32_t* past_rope, smla_stream_t stream) {
+  if (n < 0 || n > INT32_MAX || pool_rows < 0 || pool_rows > INT32_MAX || (d_qk != kLatent && d_qk != kLatent + kRope) ||
+      !std::isfinite(eps) || eps < 0.f)
+    return SMLA_ERR_BAD_SHAPE;
+  const bool roped = d_qk > kLatent;
+  // rope columns exist exactly when d_qk is 576; a rotation needs them, its positions and its table
+  if ((k_pe != nullptr) != roped && n > 0) return SMLA_ERR_NULL_PTR;
+  if (rope && (!roped || max_pos < 1)) return SMLA_ERR_BAD_SHAPE;
+  if (rope && !positions && n > 0) return SMLA_ERR_NULL_PTR;
+  if ((q_pe != nullptr) != (q != nullptr) || (q_pe && !rope)) return SMLA_ERR_NULL_PTR;
+  if (q_pe && (h_q < 1 || h_q > 1024)) return SMLA_ERR_BAD_SHAPE;
+  if (n == 0) return SMLA_OK;
+  if (!c_kv || !slots || (pool_rows > 0 && !kv_pool)) return SMLA_ERR_NULL_PTR;
+  if (c_stride < 0 || k_stride < 0 || q_stride_t < 0 || q_stride_h < 0) return SMLA_ERR_BAD_SHAPE;
+  if (!aligned_to(c_kv, 16) || c_stride % 8 || !aligned_to(k_pe, 4) || k_stride % 2 || !aligned_to(norm_weight, 16) ||
+      !aligned_to(rope, 16) || !aligned_to(q_pe, 16) || q_stride_t % 8 || q_stride_h % 8 || !aligned_to(q, 16) ||
+      !aligned_to(kv_pool, 16) || !aligned_to(slots, 4) || !aligned_to(positions, 4) || !aligned_to(past_rope, 4))
+    return SMLA_ERR_MISALIGNED;
+  // rows are written while others are still read; the queries' columns may be turned where they are
+  const size_t pool_bytes = static_cast<size_t>(pool_rows) * d_qk * 2;
+  const size_t q_bytes = static_cast<size_t>(n) * (q ? h_q : 0) * d_qk * 2;
+  const size_t c_bytes = (static_cast<size_t>(n - 1) * c_stride + kLatent) * 2;
+  const size_t k_bytes = (static_cast<size_t>(n - 1) * k_stride + kRope) * 2;
+  const size_t q_pe_bytes =
+      q ? (static_cast<size_t>(n - 1) * q_stride_t + static_cast<size_t>(h_q - 1) * q_stride_h + kRope) * 2 : 0;
+  const bool in_place = q_pe == static_cast<const __nv_bfloat16*>(q) + kLatent && (n == 1 || q_stride_t == int64_t{h_q} * d_qk) &&
+                        (h_q == 1 || q_stride_h == d_qk);
+  if (overlap(kv_pool, pool_bytes, c_kv, c_bytes) || overlap(kv_pool, pool_bytes, k_pe, k_bytes) ||
+      overlap(kv_pool, pool_bytes, q_pe, q_pe_bytes) || overlap(kv_pool, pool_bytes, q, q_bytes) ||
+      overlap(q, q_bytes, c_kv, c_bytes) || overlap(q, q_bytes, k_pe, k_bytes) ||
+      (!in_place && overlap(q, q_bytes, q_pe, q_pe_bytes)) || overlap(past_rope, 4, kv_pool, pool_bytes) ||
+      overlap(past_rope, 4, q, q_bytes) || overlap(past_rope, 4, slots, static_cast<size_t>(n) * 4) ||
+      overlap(past_rope, 4, rope ? positions : nullptr, static_cast<size_t>(n) * 4))
+    return SMLA_ERR_BAD_SHAPE;
+  AppendParams p{};
+  p.c_kv = static_cast<const __nv_bfloat16*>(c_kv);
+  p.k_pe = static_cast<const __nv_bfloat16*>(k_pe);
+  p.slots = slots;
+  p.positions = positions;
+  p.rope = rope;
+  p.norm_weight = static_cast<const __nv_bfloat16*>(norm_weight);
+  p.q_pe = static_cast<const __nv_bfloat16*>(q_pe);
+  p.q = static_cast<__nv_bfloat16*>(q);
+  p.pool = static_cast<__nv_bfloat16*>(kv_pool);
+  p.past_rope = past_rope;
+  p.c_stride = c_stride;
+  p.k_stride = k_stride;
+  p.q_stride_t = q_stride_t;
+  p.q_stride_h = q_stride_h;
+  p.max_pos = max_pos;
+  p.pool_rows = pool_rows;
+  p.n = n;
+  p.eps = eps;
+  p.d_qk = d_qk;
+  p.h_q = h_q;
+  p.units = 1 + (q_pe ? (h_q + kHeadsPerUnit - 1) / kHeadsPerUnit : 0);
+  const int64_t per_cta = kAppendThreads / 32;
+  const int64_t ctas = (n * p.units + per_cta - 1) / per_cta;
+  if (ctas > INT32_MAX) return SMLA_ERR_BAD_SHAPE;
+  append_kv_kernel<<<static_cast<unsigned>(ctas), kAppendThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
+  return cudaGetLastError() == cudaSuccess ? SMLA_OK : SMLA_ERR_LAUNCH;
 }
 
 }  // namespace
@@ -341,63 +412,19 @@ smla_status sparse_mla_append_kv(const void* c_kv, int64_t c_stride, const void*
                                  const void* norm_weight, float eps, const void* q_pe, int64_t q_stride_t,
                                  int64_t q_stride_h, void* q, int h_q, void* kv_pool, int64_t pool_rows, int d_qk,
                                  int64_t n, smla_stream_t stream) {
-  if (n < 0 || n > INT32_MAX || pool_rows < 0 || pool_rows > INT32_MAX || (d_qk != kLatent && d_qk != kLatent + kRope) ||
-      !std::isfinite(eps) || eps < 0.f)
-    return SMLA_ERR_BAD_SHAPE;
-  const bool roped = d_qk > kLatent;
-  // rope columns exist exactly when d_qk is 576; a rotation needs them, its positions and its table
-  if ((k_pe != nullptr) != roped && n > 0) return SMLA_ERR_NULL_PTR;
-  if (rope && (!roped || max_pos < 1)) return SMLA_ERR_BAD_SHAPE;
-  if (rope && !positions && n > 0) return SMLA_ERR_NULL_PTR;
-  if ((q_pe != nullptr) != (q != nullptr) || (q_pe && !rope)) return SMLA_ERR_NULL_PTR;
-  if (q_pe && (h_q < 1 || h_q > 1024)) return SMLA_ERR_BAD_SHAPE;
-  if (n == 0) return SMLA_OK;
-  if (!c_kv || !slots || (pool_rows > 0 && !kv_pool)) return SMLA_ERR_NULL_PTR;
-  if (c_stride < 0 || k_stride < 0 || q_stride_t < 0 || q_stride_h < 0) return SMLA_ERR_BAD_SHAPE;
-  if (!aligned_to(c_kv, 16) || c_stride % 8 || !aligned_to(k_pe, 4) || k_stride % 2 || !aligned_to(norm_weight, 16) ||
-      !aligned_to(rope, 16) || !aligned_to(q_pe, 16) || q_stride_t % 8 || q_stride_h % 8 || !aligned_to(q, 16) ||
-      !aligned_to(kv_pool, 16) || !aligned_to(slots, 4) || !aligned_to(positions, 4))
-    return SMLA_ERR_MISALIGNED;
-  // rows are written while others are still read; the queries' columns may be turned where they are
-  const size_t pool_bytes = static_cast<size_t>(pool_rows) * d_qk * 2;
-  const size_t q_bytes = static_cast<size_t>(n) * (q ? h_q : 0) * d_qk * 2;
-  const size_t c_bytes = (static_cast<size_t>(n - 1) * c_stride + kLatent) * 2;
-  const size_t k_bytes = (static_cast<size_t>(n - 1) * k_stride + kRope) * 2;
-  const size_t q_pe_bytes =
-      q ? (static_cast<size_t>(n - 1) * q_stride_t + static_cast<size_t>(h_q - 1) * q_stride_h + kRope) * 2 : 0;
-  const bool in_place = q_pe == static_cast<const __nv_bfloat16*>(q) + kLatent && (n == 1 || q_stride_t == int64_t{h_q} * d_qk) &&
-                        (h_q == 1 || q_stride_h == d_qk);
-  if (overlap(kv_pool, pool_bytes, c_kv, c_bytes) || overlap(kv_pool, pool_bytes, k_pe, k_bytes) ||
-      overlap(kv_pool, pool_bytes, q_pe, q_pe_bytes) || overlap(kv_pool, pool_bytes, q, q_bytes) ||
-      overlap(q, q_bytes, c_kv, c_bytes) || overlap(q, q_bytes, k_pe, k_bytes) ||
-      (!in_place && overlap(q, q_bytes, q_pe, q_pe_bytes)))
-    return SMLA_ERR_BAD_SHAPE;
-  AppendParams p{};
-  p.c_kv = static_cast<const __nv_bfloat16*>(c_kv);
-  p.k_pe = static_cast<const __nv_bfloat16*>(k_pe);
-  p.slots = slots;
-  p.positions = positions;
-  p.rope = rope;
-  p.norm_weight = static_cast<const __nv_bfloat16*>(norm_weight);
-  p.q_pe = static_cast<const __nv_bfloat16*>(q_pe);
-  p.q = static_cast<__nv_bfloat16*>(q);
-  p.pool = static_cast<__nv_bfloat16*>(kv_pool);
-  p.c_stride = c_stride;
-  p.k_stride = k_stride;
-  p.q_stride_t = q_stride_t;
-  p.q_stride_h = q_stride_h;
-  p.max_pos = max_pos;
-  p.pool_rows = pool_rows;
-  p.n = n;
-  p.eps = eps;
-  p.d_qk = d_qk;
-  p.h_q = h_q;
-  p.units = 1 + (q_pe ? (h_q + kHeadsPerUnit - 1) / kHeadsPerUnit : 0);
-  const int64_t per_cta = kAppendThreads / 32;
-  const int64_t ctas = (n * p.units + per_cta - 1) / per_cta;
-  if (ctas > INT32_MAX) return SMLA_ERR_BAD_SHAPE;
-  append_kv_kernel<<<static_cast<unsigned>(ctas), kAppendThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
-  return cudaGetLastError() == cudaSuccess ? SMLA_OK : SMLA_ERR_LAUNCH;
+  return append_kv(c_kv, c_stride, k_pe, k_stride, slots, positions, rope, max_pos, norm_weight, eps, q_pe, q_stride_t,
+                   q_stride_h, q, h_q, kv_pool, pool_rows, d_qk, n, nullptr, stream);
+}
+
+smla_status sparse_mla_append_kv_counted(const void* c_kv, int64_t c_stride, const void* k_pe, int64_t k_stride,
+                                         const int32_t* slots, const int32_t* positions, const float* rope,
+                                         int64_t max_pos, const void* norm_weight, float eps, const void* q_pe,
+                                         int64_t q_stride_t, int64_t q_stride_h, void* q, int h_q, void* kv_pool,
+                                         int64_t pool_rows, int d_qk, int64_t n, int32_t* past_rope,
+                                         smla_stream_t stream) {
+  if (!past_rope) return SMLA_ERR_NULL_PTR;
+  return append_kv(c_kv, c_stride, k_pe, k_stride, slots, positions, rope, max_pos, norm_weight, eps, q_pe, q_stride_t,
+                   q_stride_h, q, h_q, kv_pool, pool_rows, d_qk, n, past_rope, stream);
 }
 
 }  // extern "C"

@@ -135,3 +135,21 @@ def test_wrappers_reject_wrong_tensors():
         smla.sparse_mla_chunk_fwd_paged(b, b, i.view(2, 2), i, i)
     with pytest.raises(TypeError):
         smla.sparse_mla_chunk_fwd_paged(b.float(), b, i.view(2, 2), i, i)
+
+
+def test_counted_append_refusals(lib):
+    def call(past, **kw):
+        a = dict(c=FAKE, k=FAKE + STEP, pool=FAKE + 8 * STEP, n=5)
+        a.update(kw)
+        return lib.sparse_mla_append_kv_counted(
+            a["c"], 576, a["k"], 576, FAKE + 2 * STEP, FAKE + 3 * STEP, FAKE + 4 * STEP, 100, None, ctypes.c_float(1e-6),
+            FAKE + 6 * STEP, 24 * 64, 64, FAKE + 7 * STEP, 24, a["pool"], 128, 576, a["n"], past, None)
+
+    free = FAKE + 9 * STEP
+    assert call(None) == NULL
+    assert call(free + 2) == MISALIGNED
+    assert call(FAKE + 8 * STEP + 128 * 1152 - 4) == SHAPE     # the cache's last bytes
+    assert call(FAKE + 7 * STEP + 1024) == SHAPE               # the queries'
+    assert call(FAKE + 2 * STEP + 16) == SHAPE and call(FAKE + 3 * STEP) == SHAPE   # slots, positions
+    assert call(free, c=None) == NULL and call(free, pool=FAKE + 4096) == SHAPE
+    assert call(free, n=0) == 0

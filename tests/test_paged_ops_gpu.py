@@ -667,3 +667,40 @@ def test_chunk_nan_does_not_hide_empty_rows():
     for rows in (slice(0, 3), slice(5, 8)):
         assert bool((out[rows] == 0).all()) and bool((lse[rows] == float("inf")).all()) and bool((top[rows] == float("-inf")).all())
     assert all(bool(x[3:5].isnan().all()) for x in (out, lse, top))
+
+
+def test_a_request_that_outgrows_the_rope_table():
+    """Plan, append and attend across the end of the rope table: the tokens behind it are counted, call after call and
+    in a replayed graph; with a table for every position of the block table no row that is read stays unwritten."""
+    torch.manual_seed(6)
+    heads, page, width, n = 16, 16, 4, 90
+    lens, new = i32([30, 0, 61]), i32([20, 64, 5])     # positions to 49, 63 and 65: the last two past the block table
+    x, q = torch.randn(n, 576, device="cuda").to(torch.bfloat16), torch.randn(n, heads, 576, device="cuda").to(torch.bfloat16)
+    for max_pos, past in ((64, 2), (40, 10 + 24 + 5), (66, 0), (63, 1 + 3)):
+        table = i32([[0, 1, -1, -1], [-1] * 4, [2, 3, 4, 5]])
+        pool = torch.full((20 * page, 1, 576), float("nan"), dtype=torch.bfloat16, device="cuda")
+        k, cu, slots, pos, counts = smla.sparse_mla_plan_pages(lens, new, table, i32(np.arange(6, 20)), n, page_block=page)
+        old = torch.cat([table[0, :2].long()[:, None] * page + torch.arange(page, device="cuda"),
+                         table[2].long()[:, None] * page + torch.arange(page, device="cuda")]).flatten()
+        pool[old] = 1.0
+        pool[slots[slots >= 0].long()] = float("nan")
+        beyond, turned = torch.zeros(1, dtype=torch.int32, device="cuda"), q.clone()
+        args = dict(c_kv=x[:, :512], k_pe=x[:, 512:], slots=slots, kv_pool=pool, positions=pos, rope=rope_table(max_pos),
+                    q_pe=q[..., 512:], q=turned)
+        smla.sparse_mla_append_kv(**args, past_rope=beyond)
+        assert int(beyond) == past
+        smla.sparse_mla_append_kv(**args, past_rope=beyond, stream=torch.cuda.Stream())
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            smla.sparse_mla_append_kv(**args, past_rope=beyond)
+        graph.replay()
+        assert int(beyond) == 3 * past
+        written = int((~pool[slots[slots >= 0].long(), 0].isnan().any(-1)).sum())
+        assert written == int(((pos >= 0) & (pos < max_pos) & (slots >= 0)).sum())
+        if max_pos >= width * page:
+            chunk_check(dict(q=turned, kv_pool=pool, block_table=table, cu_seqlens_q=cu, seqlens_k=k, page_block=page))
+    with pytest.raises(ValueError):
+        smla.sparse_mla_append_kv(**args, past_rope=i32([0, 0]))
+    with pytest.raises(smla.SmlaError):
+        smla.sparse_mla_append_kv(**args, past_rope=pool.view(torch.int32).view(-1)[:1])
