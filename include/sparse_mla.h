@@ -299,6 +299,7 @@ smla_status sparse_mla_plan_pages(const int32_t* seqlens, const int32_t* new_len
  *                16-byte aligned, or NULL; needs rope.  It may be q[..., 512:] itself.
  *   q            [n, h_q, 576] bf16, 16-byte aligned; given exactly when q_pe is
  *   kv_pool      [pool_rows, d_qk] bf16, 16-byte aligned
+ * A stride over a single token (n == 1) or head (h_q == 1) is not looked at.
  * Arithmetic is fp32, each value is rounded to bf16 once; without a norm weight (without rope) the
  * bits are copied.  Two tokens with one slot leave that row undefined.  SMLA_ERR_BAD_SHAPE when
  * kv_pool overlaps c_kv, k_pe, q_pe or q, or q overlaps c_kv, k_pe or, other than in place, q_pe.

@@ -489,8 +489,8 @@ def sparse_mla_append_kv(c_kv, k_pe, slots, kv_pool, norm_weight=None, eps=1e-6,
     number of such tokens (a table of max_blocks * page_block positions covers every row that the
     planner gives).  With q_pe [n, h, 64] bf16, q[..., 512:] of q
     [n, h, 576] gets the queries' columns turned by the same angles.  c_kv, k_pe and q_pe may be
-    strided views (slices of a projection's output) with a contiguous last dimension.  Returns
-    kv_pool."""
+    strided views (slices of a projection's output) with a contiguous last dimension, the other strides
+    even for k_pe and multiples of eight for c_kv and q_pe.  Returns kv_pool."""
     lib = load_library()
     bf16 = torch.bfloat16
     dev = _dense(kv_pool, "kv_pool", bf16)

@@ -315,6 +315,9 @@ smla_status append_kv(const void* c_kv, int64_t c_stride, const void* k_pe, int6
   if (q_pe && (h_q < 1 || h_q > 1024)) return SMLA_ERR_BAD_SHAPE;
   if (n == 0) return SMLA_OK;
   if (!c_kv || !slots || (pool_rows > 0 && !kv_pool)) return SMLA_ERR_NULL_PTR;
+  // the stride of a single token or head addresses nothing, whatever it is
+  if (n == 1) c_stride = k_stride = q_stride_t = 0;
+  if (h_q == 1) q_stride_h = 0;
   if (c_stride < 0 || k_stride < 0 || q_stride_t < 0 || q_stride_h < 0) return SMLA_ERR_BAD_SHAPE;
   if (!aligned_to(c_kv, 16) || c_stride % 8 || !aligned_to(k_pe, 4) || k_stride % 2 || !aligned_to(norm_weight, 16) ||
       !aligned_to(rope, 16) || !aligned_to(q_pe, 16) || q_stride_t % 8 || q_stride_h % 8 || !aligned_to(q, 16) ||

@@ -153,3 +153,12 @@ def test_counted_append_refusals(lib):
     assert call(FAKE + 2 * STEP + 16) == SHAPE and call(FAKE + 3 * STEP) == SHAPE   # slots, positions
     assert call(free, c=None) == NULL and call(free, pool=FAKE + 4096) == SHAPE
     assert call(free, n=0) == 0
+
+
+def test_strides_of_one_token_or_head_are_not_looked_at(lib):
+    """With the strides accepted, each call comes to the overlap check, which refuses it."""
+    over = dict(pool=FAKE)
+    assert append(lib, n=1, cs=1, ks=1, qt=-3, qh=64, **over) == SHAPE
+    assert append(lib, h=1, qh=1, qt=64, **over) == SHAPE
+    assert append(lib, n=1, h=1, cs=5, ks=5, qt=5, qh=5, **over) == SHAPE
+    assert append(lib, n=2, cs=5, **over) == MISALIGNED and append(lib, h=2, qh=5, **over) == MISALIGNED

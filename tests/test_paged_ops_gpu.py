@@ -704,3 +704,26 @@ def test_a_request_that_outgrows_the_rope_table():
         smla.sparse_mla_append_kv(**args, past_rope=i32([0, 0]))
     with pytest.raises(smla.SmlaError):
         smla.sparse_mla_append_kv(**args, past_rope=pool.view(torch.int32).view(-1)[:1])
+
+
+def test_append_of_one_token_or_head_with_any_stride():
+    """A projection of one column vector, transposed, is contiguous and has the strides (1, 1)."""
+    torch.manual_seed(7)
+    up, hidden = torch.randn(576 + 192, 64, device="cuda").to(torch.bfloat16), torch.randn(64, 1, device="cuda").to(torch.bfloat16)
+    y = (up @ hidden).t()
+    assert y.stride() == (1, 1)
+    slots, pos, rope = i32([3]), i32([5]), rope_table(9)
+    got = []
+    for c_stride, k_stride, q_stride in ((1, 3, 7), (512, 64, 192)):
+        pool, q = torch.zeros(8, 1, 576, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, 3, 576, dtype=torch.bfloat16, device="cuda")
+        smla.sparse_mla_append_kv(y[:, :512].as_strided((1, 512), (c_stride, 1)), y[:, 512:576].as_strided((1, 64), (k_stride, 1)),
+                                  slots, pool, positions=pos, rope=rope, q_pe=y[:, 576:].as_strided((1, 3, 64), (q_stride, 64, 1)), q=q)
+        got.append((pool, q))
+    assert all(torch.equal(a, b) for a, b in zip(*got)) and int((got[0][0] != 0).any(-1).sum()) == 1
+    x, one = torch.randn(4, 576, device="cuda").to(torch.bfloat16), torch.randn(4, 1, 64, device="cuda").to(torch.bfloat16)
+    got = []
+    for qp in (one, one.as_strided((4, 1, 64), (64, 3, 1))):
+        pool, q = torch.zeros(8, 1, 576, dtype=torch.bfloat16, device="cuda"), torch.zeros(4, 1, 576, dtype=torch.bfloat16, device="cuda")
+        smla.sparse_mla_append_kv(x[:, :512], x[:, 512:], i32([0, 1, 2, 7]), pool, positions=i32([0, 1, 8, 3]), rope=rope, q_pe=qp, q=q)
+        got.append((pool, q))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
