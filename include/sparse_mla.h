@@ -349,7 +349,8 @@ smla_status sparse_mla_append_kv_counted(const void* c_kv, int64_t c_stride, con
  *   workspace     device buffer of at least sparse_mla_chunk_workspace_size(n_tok, h_q) bytes,
  *                 256-byte aligned, owned by the caller; needs no initialisation, its contents
  *                 are meaningless after the call.  Two calls in flight at once must not share it.
- * q, kv_pool and out are 16-byte aligned, the rest 4-byte.  The result does not depend on
+ * q, kv_pool and out are 16-byte aligned, the rest 4-byte.  SMLA_ERR_BAD_SHAPE when out, lse,
+ * max_logits or the workspace overlaps an input or another of them.  The result does not depend on
  * anything but the arguments (no atomics): two calls give the same bits.
  * n_tok == 0 or n_req == 0 is a no-op.
  */

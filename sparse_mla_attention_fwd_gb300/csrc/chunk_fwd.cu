@@ -1080,6 +1080,13 @@ smla_status sparse_mla_chunk_fwd_paged(const void* q, const void* kv_pool, int64
   const Workspace ws = workspace_of(n_tok, h_q);
   if (!workspace || workspace_bytes < ws.bytes) return SMLA_ERR_WORKSPACE;
   if (!aligned_to(workspace, 256)) return SMLA_ERR_MISALIGNED;
+  // tiles are finished, and parts stored, while other CTAs still read the inputs
+  const size_t rows = static_cast<size_t>(n_tok) * h_q, reqs = static_cast<size_t>(n_req) * 4;
+  const Span in[] = {{q, rows * d_qk * 2}, {kv_pool, static_cast<size_t>(pool_rows) * d_qk * 2},
+                     {block_table, reqs * max_blocks}, {cu_seqlens_q, reqs + 4}, {seqlens_k, reqs},
+                     {attn_sink, static_cast<size_t>(h_q) * 4}};
+  const Span written[] = {{out, rows * kDv * 2}, {lse, rows * 4}, {max_logits, rows * 4}, {workspace, ws.bytes}};
+  if (any_overlap(in, written)) return SMLA_ERR_BAD_SHAPE;
   const int sms = device_sms();
   if (sms < 2) return SMLA_ERR_LAUNCH;
   ChunkParams p{};

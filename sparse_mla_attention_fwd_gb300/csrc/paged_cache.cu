@@ -392,16 +392,10 @@ smla_status sparse_mla_plan_pages(const int32_t* seqlens, const int32_t* new_len
     if (!aligned_to(x, 4)) return SMLA_ERR_MISALIGNED;
   // the CTAs read the inputs while others write the outputs: those must be other memory
   const size_t rb = static_cast<size_t>(n_req) * 4, tb = static_cast<size_t>(n_tokens) * 4;
-  const struct { const void* p; size_t n; } in[] = {{seqlens, rb}, {new_lens, rb}, {free_start, 4},
-                                                    {free_pages, static_cast<size_t>(n_free) * 4}};
-  const struct { const void* p; size_t n; } out[] = {{block_table, rb * max_blocks}, {seqlens_k, rb},
-                                                     {cu_seqlens_q, rb + 4}, {slots, tb}, {positions, tb}, {counts, 12}};
-  for (const auto& o : out) {
-    for (const auto& i : in)
-      if (overlap(o.p, o.n, i.p, i.n)) return SMLA_ERR_BAD_SHAPE;
-    for (const auto& o2 : out)
-      if (&o != &o2 && overlap(o.p, o.n, o2.p, o2.n)) return SMLA_ERR_BAD_SHAPE;
-  }
+  const Span in[] = {{seqlens, rb}, {new_lens, rb}, {free_start, 4}, {free_pages, static_cast<size_t>(n_free) * 4}};
+  const Span written[] = {{block_table, rb * max_blocks}, {seqlens_k, rb}, {cu_seqlens_q, rb + 4},
+                          {slots, tb}, {positions, tb}, {counts, 12}};
+  if (any_overlap(in, written)) return SMLA_ERR_BAD_SHAPE;
   PlanParams p{seqlens, new_lens, block_table, free_pages, free_start, seqlens_k, cu_seqlens_q, slots, positions,
                counts, n_req, n_free, static_cast<int32_t>(n_tokens), max_blocks, page_block};
   int64_t ctas = (n_tokens + kPlanThreads - 1) / kPlanThreads;

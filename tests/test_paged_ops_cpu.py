@@ -162,3 +162,16 @@ def test_strides_of_one_token_or_head_are_not_looked_at(lib):
     assert append(lib, h=1, qh=1, qt=64, **over) == SHAPE
     assert append(lib, n=1, h=1, cs=5, ks=5, qt=5, qh=5, **over) == SHAPE
     assert append(lib, n=2, cs=5, **over) == MISALIGNED and append(lib, h=2, qh=5, **over) == MISALIGNED
+
+
+APART = {n: FAKE + (i << 28) for i, n in enumerate(("q", "pool", "table", "cu", "seqlens", "sink", "out", "lse", "mx", "ws"))}
+SIZES = dict(q=9 * 128 * 1152, pool=4096 * 1152, table=3 * 64 * 4, cu=16, seqlens=12, sink=512, out=9 * 128 * 1024, lse=9 * 128 * 4,
+             mx=9 * 128 * 4, ws=160 * 128 * 2048)
+
+
+@pytest.mark.parametrize("written,other", [(a, b) for a in ("out", "lse", "mx", "ws") for b in APART if a != b])
+def test_chunk_refuses_overlapping_buffers(lib, written, other):
+    size = SIZES[other] - SIZES[other] % 256 or 256
+    at = [APART[other], APART[other] + size - 256]      # on its first bytes, and on its last
+    for a in at:
+        assert chunk(lib, **dict(APART, **{written: a})) == SHAPE

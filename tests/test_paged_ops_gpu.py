@@ -727,3 +727,20 @@ def test_append_of_one_token_or_head_with_any_stride():
         smla.sparse_mla_append_kv(x[:, :512], x[:, 512:], i32([0, 1, 2, 7]), pool, positions=i32([0, 1, 8, 3]), rope=rope, q_pe=qp, q=q)
         got.append((pool, q))
     assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+def test_chunk_buffers_may_touch_and_not_overlap():
+    w = chunk_case(24, [2, 1], [700, 90], 16, 512)
+    want = smla.sparse_mla_chunk_fwd_paged(**w)
+    rows, need = 3 * 16, smla.load_library().sparse_mla_chunk_workspace_size(3, 16)
+    block = torch.empty(need + rows * (1024 + 1024 + 8), dtype=torch.uint8, device="cuda")
+    ws, q, out, lse, top = block.split([need, rows * 1024, rows * 1024, rows * 4, rows * 4])
+    q, out = q.view(torch.bfloat16).view(3, 16, 512), out.view(torch.bfloat16).view(3, 16, 512)
+    lse, top = lse.view(torch.float32).view(3, 16), top.view(torch.float32).view(3, 16)
+    q.copy_(w["q"])
+    w["q"] = q
+    got = smla.sparse_mla_chunk_fwd_paged(**w, out=out, lse=lse, max_logits=top, workspace=ws)
+    assert all(torch.equal(a, b) for a, b in zip(want, got)) and torch.equal(got[0], out)
+    for kw in (dict(out=q), dict(lse=top), dict(workspace=block[256:256 + need]), dict(out=w["kv_pool"][:rows].view(3, 16, 512))):
+        with pytest.raises(smla.SmlaError):
+            smla.sparse_mla_chunk_fwd_paged(**w, **dict(dict(out=out, lse=lse, max_logits=top, workspace=ws), **kw))
