@@ -366,6 +366,12 @@ smla_status sparse_mla_chunk_fwd_paged(const void* q, const void* kv_pool, int64
 /* sparse_mla_device_status of sparse_mla_chunk_fwd_paged's kernel, which has its own word. */
 smla_status sparse_mla_chunk_device_status(int reset);
 
+/*
+ * sparse_mla_selftest_wait_timeout of that kernel's waits: its two forms give up after limit_ns each, a third
+ * wait at once on the flag that the first has set; the chunk kernel's status word says so.
+ */
+smla_status sparse_mla_chunk_selftest_wait_timeout(uint64_t limit_ns, smla_stream_t stream);
+
 /* Static, human-readable description of a status code.  Never NULL. */
 const char* sparse_mla_status_string(smla_status status);
 

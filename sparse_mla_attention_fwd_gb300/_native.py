@@ -19,8 +19,8 @@ EXPORTED = ("sparse_mla_fwd", "sparse_mla_fwd_paged", "sparse_mla_splitkv_worksp
             "sparse_mla_fwd_splitkv", "sparse_mla_fwd_paged_splitkv", "sparse_mla_fwd_paged_splitkv_static",
             "sparse_mla_fwd_host", "sparse_mla_selftest_wait_timeout", "sparse_mla_device_status",
             "sparse_mla_status_string", "sparse_mla_abi_version", "sparse_mla_bwd", "sparse_mla_plan_pages",
-            "sparse_mla_append_kv", "sparse_mla_append_kv_counted", "sparse_mla_chunk_workspace_size", "sparse_mla_chunk_fwd_paged",
-            "sparse_mla_chunk_device_status")
+            "sparse_mla_append_kv", "sparse_mla_append_kv_counted", "sparse_mla_chunk_workspace_size",
+            "sparse_mla_chunk_fwd_paged", "sparse_mla_chunk_device_status", "sparse_mla_chunk_selftest_wait_timeout")
 
 _lock = threading.Lock()
 _lib = None
@@ -92,6 +92,8 @@ def load_library(path: str | None = None):
                                                    I32, I32, P, SZ, P]
         lib.sparse_mla_chunk_device_status.restype = I32
         lib.sparse_mla_chunk_device_status.argtypes = [I32]
+        lib.sparse_mla_chunk_selftest_wait_timeout.restype = I32
+        lib.sparse_mla_chunk_selftest_wait_timeout.argtypes = [ctypes.c_uint64, P]
         _lib = lib
         return lib
 

@@ -229,7 +229,8 @@ __device__ __forceinline__ void give_up(volatile int* abort) {
 
 // The clock and the abort flag are looked at every 16 tries: with both in every try the kernel is 2 % slower.
 template <bool PAIR>
-__device__ __forceinline__ void wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort) {
+__device__ __forceinline__ void wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                             uint64_t limit_ns = kWaitLimitNs) {
   constexpr uint32_t kSleepNs = 100000;
   const uint32_t a = smem_u32(bar);
   auto done = [&] { return PAIR ? mbar_sleep_cluster(a, parity, kSleepNs) : mbar_sleep(a, parity, kSleepNs); };
@@ -237,7 +238,7 @@ __device__ __forceinline__ void wait_bounded(uint64_t* bar, uint32_t parity, vol
   const uint64_t t0 = globaltimer_ns();
   uint32_t tries = 0;
   while (!done())
-    if ((++tries & 15u) == 0u && (*abort || globaltimer_ns() - t0 > kWaitLimitNs)) return give_up(abort);
+    if ((++tries & 15u) == 0u && (*abort || globaltimer_ns() - t0 > limit_ns)) return give_up(abort);
 }
 __device__ __forceinline__ void wait_on(uint64_t* bar, uint32_t parity, volatile int* abort) {
   wait_bounded<false>(bar, parity, abort);
@@ -959,6 +960,21 @@ __global__ void __launch_bounds__(32 * kJoinWarps) chunk_join_kernel(const Chunk
     if (lane < 16) reinterpret_cast<uint2*>(p.out + (static_cast<int64_t>(join.x) + row0 + k) * kDv + 64 * blockIdx.z)[lane] = tile[k][lane];
 }
 
+// ------------------------------------------------------------------------ wait self-test
+// Both forms of the wait, on a barrier that nothing completes: each gives up after limit_ns.  A third one finds the
+// flag of the first set and gives up at once, whatever its limit.
+__global__ void chunk_wait_selftest_kernel(uint64_t limit_ns) {
+  __shared__ __align__(8) uint64_t bar;
+  __shared__ int abort_flag[2];
+  if (threadIdx.x != 0) return;
+  abort_flag[0] = abort_flag[1] = 0;
+  mbar_init(smem_u32(&bar), 1);
+  fence_mbar_init();
+  wait_bounded<false>(&bar, 0, &abort_flag[0], limit_ns);
+  wait_bounded<true>(&bar, 0, &abort_flag[1], limit_ns);
+  wait_bounded<false>(&bar, 0, &abort_flag[0]);
+}
+
 // ------------------------------------------------------------------------ host side
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -1122,6 +1138,12 @@ smla_status sparse_mla_chunk_fwd_paged(const void* q, const void* kv_pool, int64
   const int pairs = sms / 2 < kMaxPairs ? sms / 2 : kMaxPairs;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return d_qk == 512 ? launch<512>(qm, hm, bm, gm, rm, p, pairs, s) : launch<576>(qm, hm, bm, gm, rm, p, pairs, s);
+}
+
+smla_status sparse_mla_chunk_selftest_wait_timeout(uint64_t limit_ns, smla_stream_t stream) {
+  if (limit_ns == 0 || limit_ns > kWaitLimitNs) return SMLA_ERR_BAD_SHAPE;
+  chunk_wait_selftest_kernel<<<1, 32, 0, reinterpret_cast<cudaStream_t>(stream)>>>(limit_ns);
+  return cudaGetLastError() == cudaSuccess ? SMLA_OK : SMLA_ERR_LAUNCH;
 }
 
 smla_status sparse_mla_chunk_device_status(int reset) {

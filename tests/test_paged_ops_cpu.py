@@ -175,3 +175,8 @@ def test_chunk_refuses_overlapping_buffers(lib, written, other):
     at = [APART[other], APART[other] + size - 256]      # on its first bytes, and on its last
     for a in at:
         assert chunk(lib, **dict(APART, **{written: a})) == SHAPE
+
+
+def test_wait_selftest_refuses_limits_out_of_range(lib):
+    for limit in (0, 2_000_000_001, 2 ** 64 - 1):
+        assert lib.sparse_mla_chunk_selftest_wait_timeout(limit, None) == SHAPE

@@ -744,3 +744,26 @@ def test_chunk_buffers_may_touch_and_not_overlap():
     for kw in (dict(out=q), dict(lse=top), dict(workspace=block[256:256 + need]), dict(out=w["kv_pool"][:rows].view(3, 16, 512))):
         with pytest.raises(smla.SmlaError):
             smla.sparse_mla_chunk_fwd_paged(**w, **dict(dict(out=out, lse=lse, max_logits=top, workspace=ws), **kw))
+
+
+def test_chunk_waits_give_up_and_report_it():
+    """A wait that runs out is reported by the chunk kernel's word and by the Python function, until it is reset; the
+    other kernels' word stays clear, and the next call is right."""
+    lib, limit = smla.load_library(), 20_000_000
+    assert smla.sparse_mla_device_status(reset=True) == 0
+    e = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    stream = torch.cuda.current_stream()
+    e[0].record(stream)
+    assert lib.sparse_mla_chunk_selftest_wait_timeout(limit, stream.cuda_stream) == 0
+    e[1].record(stream)
+    torch.cuda.synchronize()
+    # two waits of the limit, 16 tries of 0.1 ms after it at most; the third at once instead of after its 2 s
+    assert 40.0 <= e[0].elapsed_time(e[1]) < 1000.0
+    assert lib.sparse_mla_device_status(0) == 0 and lib.sparse_mla_chunk_device_status(0) == 5
+    assert smla.sparse_mla_device_status() == 5
+    assert smla.sparse_mla_device_status(reset=True) == 5
+    assert smla.sparse_mla_device_status() == 0 and lib.sparse_mla_chunk_device_status(0) == 0
+    assert lib.sparse_mla_selftest_wait_timeout(limit, None) == 0      # the other word, by the same function
+    torch.cuda.synchronize()
+    assert lib.sparse_mla_chunk_device_status(0) == 0 and smla.sparse_mla_device_status(reset=True) == 5
+    chunk_check(chunk_case(25, [2, 1], [700, 90], 16))
