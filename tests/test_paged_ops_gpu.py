@@ -767,3 +767,31 @@ def test_chunk_waits_give_up_and_report_it():
     torch.cuda.synchronize()
     assert lib.sparse_mla_chunk_device_status(0) == 0 and smla.sparse_mla_device_status(reset=True) == 5
     chunk_check(chunk_case(25, [2, 1], [700, 90], 16))
+
+
+@pytest.mark.parametrize("heads,n_k", [(16, 700), (128, 2600), (20, 9000)])
+def test_chunk_large_scores_that_are_exact(heads, n_k):
+    """Scores of a thousand and more from small whole numbers, whose products and sums fp32 holds exactly: what is left are
+    the roundings of the softmax.  Later keys are longer, so the running maximum moves far, block after block."""
+    w = chunk_case(heads, [3], [n_k], heads, page=16)
+    g = torch.Generator().manual_seed(n_k)
+    length = 1 + torch.arange(n_k) * 6 // n_k
+    keys = (torch.randint(-1, 2, (n_k, 576), generator=g) * length[:, None]).to(torch.bfloat16).cuda()
+    j = torch.arange(n_k, device="cuda")
+    w["kv_pool"][w["block_table"][0, j // 16].long() * 16 + j % 16, 0] = keys
+    w["q"] = torch.randint(-12, 13, w["q"].shape, generator=g).to(torch.bfloat16).cuda()
+    scale = 0.5
+    out, lse, top = smla.sparse_mla_chunk_fwd_paged(**w, sm_scale=scale)
+    s = torch.einsum("thd,kd->thk", w["q"].double(), keys.double()) * scale
+    s = s.masked_fill(j[None, None] > torch.arange(n_k - 3, n_k, device="cuda")[:, None, None], float("-inf"))
+    m, z = s.max(-1).values, torch.logsumexp(s, -1)
+    assert float(m.abs().max()) > 1000 and float(s[s > float("-inf")].abs().max()) < 2 ** 22
+    assert torch.equal(top.double(), m)
+    p = (s - z[..., None]).exp()
+    o, mag = torch.einsum("thk,kd->thd", p, keys[:, :512].double()), torch.einsum("thk,kd->thd", p, keys[:, :512].double().abs())
+    # The exponents are products with log2 e, and differences of such: four roundings of numbers up to 1.5 max |s|, in base 2,
+    # and each move of the running maximum, of which a row has at most one per block, rounds its own once more
+    ds = (4 + 2) * 1.5 * float(m.abs().max()) * U32 + n_k / 64 * 4 * U32
+    tol = mag * (U16 + 2.1 * ds + 2 * (n_k + 16) * U32) * (1 + U16) + o.abs() * U16 + 1e-30
+    assert bool(((out.double() - o).abs() <= tol).all())
+    assert float((lse.double() - z).abs().max()) <= ds + (n_k + 16) * U32 + 8 * U32 * float(z.abs().max()) + 8 * U32
