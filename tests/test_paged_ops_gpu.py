@@ -795,3 +795,42 @@ def test_chunk_large_scores_that_are_exact(heads, n_k):
     tol = mag * (U16 + 2.1 * ds + 2 * (n_k + 16) * U32) * (1 + U16) + o.abs() * U16 + 1e-30
     assert bool(((out.double() - o).abs() <= tol).all())
     assert float((lse.double() - z).abs().max()) <= ds + (n_k + 16) * U32 + 8 * U32 * float(z.abs().max()) + 8 * U32
+
+
+WITHOUT_SHORTCUTS = """
+import sys
+sys.path.insert(0, sys.argv[1])
+import torch
+if sys.argv[2] == "without":
+    sys.modules["torch._C._dynamo.guards"] = None
+    del torch._C._cuda_getCurrentRawStream
+import sparse_mla_attention_fwd_gb300 as smla
+assert (smla._empty_strided.__module__ == smla.__name__) == (sys.argv[2] == "without")
+assert (getattr(smla._raw_stream, "__module__", None) == smla.__name__) == (sys.argv[2] == "without")
+g = torch.Generator().manual_seed(0)
+def normal(*s):
+    return torch.randn(*s, generator=g).to(torch.bfloat16).cuda()
+pool, q, x = normal(256, 1, 576), normal(3, 16, 576), normal(3, 576)
+lens, new, free = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([100, 64], [2, 1], [3, 2]))
+table = torch.tensor([[0, 1, -1], [2, -1, -1]], dtype=torch.int32, device="cuda")
+side = torch.cuda.Stream()
+side.wait_stream(torch.cuda.current_stream())
+with torch.cuda.stream(side):
+    k, cu, slots, pos, counts = smla.sparse_mla_plan_pages(lens, new, table, free, 3)
+    smla.sparse_mla_append_kv(x[:, :512], x[:, 512:], slots, pool)
+    assert torch.equal(pool[slots.long(), 0], x)
+    got = smla.sparse_mla_chunk_fwd_paged(q, pool, table, cu, k)
+torch.cuda.synchronize()
+torch.save([t.cpu() for t in (k, cu, slots, pos, counts, pool, *got)], sys.argv[3])
+"""
+
+
+def test_wrappers_without_torchs_private_functions(tmp_path):
+    """The output allocation and the stream handle through torch's public functions: the same values."""
+    got = []
+    for mode in ("with", "without"):
+        path = str(tmp_path / mode)
+        done = subprocess.run([sys.executable, "-c", WITHOUT_SHORTCUTS, ROOT, mode, path], capture_output=True, text=True, timeout=300)
+        assert done.returncode == 0, done.stderr[-2000:]
+        got.append(torch.load(path))
+    assert len(got[0]) == 9 and all(torch.equal(a, b) for a, b in zip(*got))
