@@ -40,9 +40,9 @@
 // operands' 3 KB at 128 bytes a cycle of shared memory hold at 25 cycles instead of 16, and 8 of N = 256 at 64).
 // Arriving keys (52 KB) and P want the same shared memory: 1690 cycles if nothing ran beside the products.  The
 // L2 delivers 52 KB in 1400 (37 bytes a cycle and SM when all SMs load).  4 x 512 tokens behind 2048-8192 keys, 64
-// heads: 1676 cycles a block over the whole launch, 0.94 ms = 1460 TFLOP/s, L2 to SM 9.7 TB/s; 2048 tokens over
-// 8192 keys, 128 heads: 2.74-2.79 ms = 1465-1490 TFLOP/s; 256 tokens of one request each over 1024-4096 keys, 128
-// heads: 164 us = 5.0 TB/s.  Blocks of 128 keys (less operand traffic, two buffers instead of four) ran at the
+// heads: 1676 cycles a block over the whole launch, 0.94-0.96 ms = 1425-1460 TFLOP/s, L2 to SM 9.7 TB/s; 2048
+// tokens over 8192 keys, 128 heads: 2.79-2.83 ms = 1445-1465 TFLOP/s; 256 tokens of one request each over 1024-4096
+// keys, 128 heads: 163-166 us = 5.0 TB/s, of which 25 us are neither keys, tile ends, start nor joining.  Blocks of 128 keys (less operand traffic, two buffers instead of four) ran at the
 // same pace on chunks and 12 % slower on single tokens.  Requesting keys two to eight blocks ahead into L2
 // made single tokens 6 to 20 % slower.
 #include <cuda.h>
@@ -429,7 +429,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const float e0 = fast_exp2(fmaf(s[2 * i], scale2, neg_m));
         const float e1 = fast_exp2(fmaf(s[2 * i + 1], scale2, neg_m));
         sum += e0 + e1;
-        w[i] = pack_bf16x2(e0, e1);   // the weights of V, as the tensor unit takes them
+        // The weights of V are rounded to bf16, since the tensor unit takes both operands in one type and V is bf16:
+        // 2^-8 of a weight at most, which a sum over many keys averages (the output's whole error is 1.7e-3 to 2.1e-3
+        // of its size against 1.7e-3 for its own rounding alone).  Two products, of a weight's high and low parts, would
+        // avoid it at 1.4 times the block's time on the tensor unit.  The sum, and with it lse, takes the unrounded ones.
+        w[i] = pack_bf16x2(e0, e1);
       }
       l = fmaf(l, alpha, sum);
       // PV of the block before has read the P tile and is done with O
@@ -1124,7 +1128,10 @@ smla_status sparse_mla_chunk_fwd_paged(const void* q, const void* kv_pool, int64
   p.max_blocks = max_blocks;
   p.page_block = page_block;
   p.causal = causal != 0;
-  // tiled loads take rows of one page, in groups of eight (the 128-byte swizzle's pattern)
+  // Tiled loads take rows of one page, in groups of eight (the 128-byte swizzle's pattern): three and one for a
+  // CTA's part of a block at 32 rows, against 104 gathers of four rows where the page size is not a multiple of 8.
+  // 256 tokens over 1024-4096 keys: pages of 64 and 32 163-170 us, 16 185 us, 8 and 24 235 us, 100 473 us, 20 492 us, 1
+  // 474 us; 4 chunks of 300-512 tokens over 2048-8192 keys, in floors: 64 and 32 1.32, 16 1.64, 8 and 24 2.25, others 5.4.
   p.box = page_block % 32 == 0 ? 32 : page_block % 16 == 0 ? 16 : page_block % 8 == 0 ? 8 : 0;
   p.pool_end = static_cast<int>(pool_rows);
   p.tokens_per_tile = h_q <= kTileRows ? kTileRows / h_q : 1;

@@ -26,7 +26,7 @@ namespace {
 // chunk's running sums.  Nothing that one CTA writes is read by another: a token in a page that
 // this launch hands out computes the page from the free list instead of reading the table.
 // The work is a few loads deep: latency bounds it, not bytes, so a CTA takes about one token a thread (700 requests with
-// 41 k tokens: 8 us, with eight tokens a thread 14 us; 1024 threads and requests a chunk are no faster.  256
+// 37 k tokens: 8 us, with eight tokens a thread 14 us; 1024 threads and requests a chunk are no faster.  256
 // requests of one token: 4.3 us, 8 requests: 3.0 us).
 constexpr int kPlanThreads = 256;
 constexpr int kPlanMaxCtas = 152;
@@ -181,8 +181,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_pages_kernel(const PlanPara
 //   (x_2i, x_2i+1) -> (x_2i cos_i - x_2i+1 sin_i, x_2i+1 cos_i + x_2i sin_i),
 // cos_i, sin_i from the row of the rope table at the token's position.  The same launch turns the
 // queries' rope columns of every head into q[..., 512:].  All arithmetic is in fp32 and each value
-// is rounded to bf16 once.  The bytes bound it: every input is read once and every output written once (8192
-// tokens, 16 heads: 54 MB in 9.9 us, 5.5 TB/s; 256 tokens, 128 heads: 9 MB in 2.6 us).
+// is rounded to bf16 once.  Every input is read once and every output written once.  Latency bounds it: a
+// warp does one unit behind two dependent reads (position, then table row), and 58-60 % of the warp slots are
+// active.  8192 tokens, 16 heads, 54 MB: 12.3 us over inputs that pass the L2 (4.4 TB/s; DRAM at 27-30 % of its
+// peak in the launch, since the rows written stay in the L2), 9.8 us over two sets that it holds; 256 tokens, 128
+// heads, 9 MB: 4.2 and 2.7 us.
 // A warp takes one unit: the token's row (16 latent values a lane, the sum of squares over the
 // warp), or 16 heads of its queries (8 lanes a head, 16 bytes a lane, four loads in flight).
 constexpr int kAppendThreads = 256;
