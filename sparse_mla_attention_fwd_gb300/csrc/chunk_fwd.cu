@@ -471,8 +471,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           break;
         }
         // Without a key l is exactly 0; with one it is about 1 at least, the term of the row's largest score, or
-        // NaN.  fmaxf passes over NaN scores, so the maximum takes its NaN from the sum.
-        const bool empty = l == 0.f;
+        // NaN, or 0 with m = +inf where a finite score leaves fp32's range once scaled: lse = m + log2 0 is NaN then, and
+        // O = 0 / 0.  fmaxf passes over NaN scores, so the maximum takes its NaN from the sum.
+        const bool empty = l == 0.f && m < INFINITY;
         const float largest = empty ? -INFINITY : l == l ? top * p.sm_scale : l;
         const bool live = row < n_rows;
         float inv = 1.f;

@@ -834,3 +834,18 @@ def test_wrappers_without_torchs_private_functions(tmp_path):
         assert done.returncode == 0, done.stderr[-2000:]
         got.append(torch.load(path))
     assert len(got[0]) == 9 and all(torch.equal(a, b) for a, b in zip(*got))
+
+
+def test_chunk_scores_past_fp32_are_not_empty_rows():
+    """Finite products that the scale takes past fp32's range, whole tiles and cut ones, beside rows that see no key."""
+    for k_lens in ([70, 0], [9000, 1]):
+        w = chunk_case(26, [2, 3], k_lens, 16)
+        w["q"][:2] = w["q"][:2].abs()
+        j = torch.arange(k_lens[0], device="cuda")
+        rows = w["block_table"][0, j // 64].long() * 64 + j % 64
+        w["kv_pool"][rows] = w["kv_pool"][rows].abs() + 0.125        # every score of the first request is above 0
+        for sink in (None, torch.randn(16, device="cuda")):
+            out, lse, top = smla.sparse_mla_chunk_fwd_paged(**w, sm_scale=2.0 ** 125, attn_sink=sink)
+            assert bool(lse[:2].isnan().all()) and bool(out[:2].isnan().all())
+            assert not bool(torch.isfinite(top[:2]).any()) and not bool((top[:2] == float("-inf")).any())
+            assert bool((out[2:4] == 0).all()) and bool((lse[2:4] == float("inf")).all())
