@@ -304,7 +304,7 @@ smla_status sparse_mla_plan_pages(const int32_t* seqlens, const int32_t* new_len
  * A stride over a single token (n == 1) or head (h_q == 1) is not looked at.
  * Arithmetic is fp32, each value is rounded to bf16 once; without a norm weight (without rope) the
  * bits are copied.  Two tokens with one slot leave that row undefined.  SMLA_ERR_BAD_SHAPE when
- * kv_pool overlaps c_kv, k_pe, q_pe or q, or q overlaps c_kv, k_pe or, other than in place, q_pe.
+ * kv_pool or q overlaps an input or the other; q_pe may lie in q in its own place alone.
  * n == 0 is a no-op.
  */
 smla_status sparse_mla_append_kv(const void* c_kv, int64_t c_stride, const void* k_pe, int64_t k_stride,

@@ -335,13 +335,12 @@ smla_status append_kv(const void* c_kv, int64_t c_stride, const void* k_pe, int6
       q ? (static_cast<size_t>(n - 1) * q_stride_t + static_cast<size_t>(h_q - 1) * q_stride_h + kRope) * 2 : 0;
   const bool in_place = q_pe == static_cast<const __nv_bfloat16*>(q) + kLatent && (n == 1 || q_stride_t == int64_t{h_q} * d_qk) &&
                         (h_q == 1 || q_stride_h == d_qk);
-  if (overlap(kv_pool, pool_bytes, c_kv, c_bytes) || overlap(kv_pool, pool_bytes, k_pe, k_bytes) ||
-      overlap(kv_pool, pool_bytes, q_pe, q_pe_bytes) || overlap(kv_pool, pool_bytes, q, q_bytes) ||
-      overlap(q, q_bytes, c_kv, c_bytes) || overlap(q, q_bytes, k_pe, k_bytes) ||
-      (!in_place && overlap(q, q_bytes, q_pe, q_pe_bytes)) || overlap(past_rope, 4, kv_pool, pool_bytes) ||
-      overlap(past_rope, 4, q, q_bytes) || overlap(past_rope, 4, slots, static_cast<size_t>(n) * 4) ||
-      overlap(past_rope, 4, rope ? positions : nullptr, static_cast<size_t>(n) * 4))
-    return SMLA_ERR_BAD_SHAPE;
+  const size_t ints = static_cast<size_t>(n) * 4;
+  const Span in[] = {{c_kv, c_bytes}, {k_pe, k_bytes}, {slots, ints}, {rope ? positions : nullptr, ints},
+                     {rope, static_cast<size_t>(max_pos) * kRope * 4}, {norm_weight, kLatent * 2},
+                     {in_place ? nullptr : q_pe, q_pe_bytes}};
+  const Span written[] = {{kv_pool, pool_bytes}, {q, q_bytes}, {past_rope, 4}};
+  if (any_overlap(in, written)) return SMLA_ERR_BAD_SHAPE;
   AppendParams p{};
   p.c_kv = static_cast<const __nv_bfloat16*>(c_kv);
   p.k_pe = static_cast<const __nv_bfloat16*>(k_pe);

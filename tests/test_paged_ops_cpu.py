@@ -180,3 +180,12 @@ def test_chunk_refuses_overlapping_buffers(lib, written, other):
 def test_wait_selftest_refuses_limits_out_of_range(lib):
     for limit in (0, 2_000_000_001, 2 ** 64 - 1):
         assert lib.sparse_mla_chunk_selftest_wait_timeout(limit, None) == SHAPE
+
+
+@pytest.mark.parametrize("written", ["pool", "q"])
+@pytest.mark.parametrize("read,size", [("slots", 20), ("positions", 20), ("rope", 100 * 256), ("w", 1024)])
+def test_append_refuses_to_write_on_what_it_reads(lib, written, read, size):
+    at = {"pool": FAKE + 8 * STEP, "q": FAKE + 7 * STEP}[written]
+    end = at + {"pool": 128 * 1152, "q": 5 * 24 * 1152}[written]
+    for a in (at, end - 16, at - (size - 1) // 16 * 16):      # its first bytes, its last, and from below
+        assert append(lib, **{read: a}) == SHAPE
