@@ -27,8 +27,8 @@
  *   - Supported shapes: h_q a positive multiple of 64 (<= 1024), d_qk in {512, 576},
  *     d_v == 512, topk >= 1, sm_scale finite and > 0, s_q * h_q <= INT32_MAX.
  *   - Alignment: q and kv (or kv_pool) 16-byte aligned; every other pointer 4-byte aligned.
- *   - Page planning, row append and dense chunk attention state their own shapes (any h_q up to
- *     1024 among them), strides and alignment; those hold in place of the two rules above.
+ *   - Page planning, row append, dense chunk attention and the operators of a speculative step state their
+ *     own shapes (any h_q up to 1024 among them), strides and alignment; those hold in place of the two rules above.
  *   - Requires an sm_103a device (GB300).
  */
 #ifndef SPARSE_MLA_GB300_H_
@@ -376,6 +376,112 @@ smla_status sparse_mla_chunk_device_status(int reset);
  * wait at once on the flag that the first has set; the chunk kernel's status word says so.
  */
 smla_status sparse_mla_chunk_selftest_wait_timeout(uint64_t limit_ns, smla_stream_t stream);
+
+/*
+ * A speculative step: a request's new tokens are the nodes of a tree, node 0 its last known token and the
+ * others drafts, each behind its parent.  sparse_mla_plan_pages gives them rows, sparse_mla_plan_tree masks and
+ * positions, sparse_mla_append_kv writes the rows, sparse_mla_tree_fwd_paged attends, sparse_mla_verify_tree finds the
+ * path that is kept, and sparse_mla_commit_tree moves its rows together and gives back the pages behind them.  The
+ * host reads nothing in between.
+ *
+ * Masks and positions of the trees.  With node i of request b in row t = cu_seqlens_q[b] + i, n_b nodes and
+ * A_i = {i} and the nodes on its way up:
+ *   parents      [n_tok] int32: index of the parent within the request, below the node's own; anything else (-1)
+ *                means none: the node comes straight behind the cached tokens
+ *   cu_seqlens_q [n_req + 1], seqlens_k [n_req]: as for sparse_mla_tree_fwd_paged
+ *   tree_mask    [n_tok, mask_words] int32 (written): bit j of word w of row t is set when node 32 w + j is in A_i.
+ *                Nodes from 32 mask_words on are in no mask.
+ *   positions    [n_tok] int32 (written): seqlens_k[b] - n_b + |A_i| - 1, the position for the rotary columns
+ * Rows of no request get an empty mask and position -1.  mask_words is 1 .. 1024.  All pointers 4-byte aligned.
+ * SMLA_ERR_BAD_SHAPE when an output overlaps an input or the other output.  n_tok == 0 is a no-op.
+ */
+smla_status sparse_mla_plan_tree(const int32_t* parents, const int32_t* cu_seqlens_q, const int32_t* seqlens_k,
+                                 int32_t* tree_mask, int32_t* positions, int64_t n_req, int64_t n_tok, int mask_words,
+                                 smla_stream_t stream);
+
+/*
+ * Dense attention of the nodes of trees over a paged latent cache: sparse_mla_chunk_fwd_paged with another rule of
+ * what a token sees.  Node i of request b (n_b nodes) sees every position below seqlens_k[b] - n_b, and position
+ * seqlens_k[b] - n_b + j exactly when bit j % 32 of word j / 32 of its row of tree_mask is set (j may be above i).
+ *   tree_mask     [n_tok, mask_words] int32, mask_words 1 .. 1024; nodes from 32 mask_words on are seen by none
+ * Everything else is as there: ragged requests, page rules, workspace (sparse_mla_chunk_workspace_size), empty
+ * rows (a node that sees nothing: O = 0, lse = +inf, max_logits = -inf), NaN, rows that are left unwritten, errors.
+ * In particular every row below seqlens_k[b] must be finite, those of nodes that a token does not see among them.
+ * A causal mask (bits 0 .. i) gives the values of the causal form up to the order of its sums.
+ */
+smla_status sparse_mla_tree_fwd_paged(const void* q, const void* kv_pool, int64_t pool_rows,
+                                      const int32_t* block_table, int max_blocks, int page_block,
+                                      const int32_t* cu_seqlens_q, const int32_t* seqlens_k, int64_t n_req,
+                                      const int32_t* tree_mask, int mask_words, const float* attn_sink, float sm_scale,
+                                      int d_v, void* out, float* lse, float* max_logits, int64_t n_tok, int h_q, int d_qk,
+                                      void* workspace, size_t workspace_bytes, smla_stream_t stream);
+
+/*
+ * Verification of drafted tokens against the target's probabilities, from given random numbers.  A request's nodes
+ * lie in rows cu_seqlens_q[b] .. (clamped to [0, n_tok], as in the attention).  The walk starts at node 0; a current
+ * node's children are tried in index order, with p and q the current node's rows of target_probs and draft_probs, x a
+ * child's token and u its accept_u:
+ *   with draft_probs (children drawn independently from q):
+ *     C = 0, Z = 1, r(v) = max(p(v) - C q(v), 0) rounded to fp32; the child is kept when u q(x) Z < r(x), else
+ *     C becomes C + Z (fp32) and Z the sum of the new r
+ *   without (children chosen outright, the likeliest tokens for example):
+ *     r = p, Z = 1; the child is kept when u Z < r(x), else Z becomes Z - r(x) and r(x) 0
+ *   A child that is kept becomes the current node.
+ * When no child is left, or max_keep nodes are kept, the request's last token is drawn from the current r: the first v
+ * with r(0) + .. + r(v) > sample_u[b] * sum r (the last v with r(v) > 0 where rounding leaves none; with r all zero,
+ * p's; -1 when p has no positive value).  The tokens kept and drawn follow the target's distribution, whatever the
+ * drafts.  Sums of r, Z and the comparisons are in 64 bits (in effect: products of two fp32 numbers are exact).
+ *   target_probs [n_tok, vocab] fp32, row stride target_stride elements (>= vocab); rows sum to 1; NaN and negative
+ *                values count as 0
+ *   draft_probs  [n_tok, vocab] fp32, row stride draft_stride, or NULL; row t is what node t's children were drawn
+ *                from (rows of nodes without children are not read); values >= 0
+ *   tokens       [n_tok] int32; a child whose token lies outside [0, vocab) is passed over
+ *   parents      [n_tok] int32 as for sparse_mla_plan_tree; a node without a parent is never tried (node 0 apart)
+ *   accept_u     [n_tok] fp32, sample_u [n_req] fp32: numbers in [0, 1)
+ *   keep         [n_req, max_keep] int32 (written): node 0 and the kept nodes, in order; -1 behind them
+ *   out_tokens   [n_req, max_keep] int32 (written): the kept drafts' tokens and the drawn one; -1 behind them
+ *   n_keep       [n_req] int32 (written): entries of both; 0 for a request without nodes
+ * Nodes of a request from 1024 on are not tried.  max_keep >= 1, n_req * max_keep <= INT32_MAX.  All pointers
+ * 4-byte aligned.  The stride of a single row is not looked at.  SMLA_ERR_BAD_SHAPE when an output overlaps an
+ * input or another output.  The same inputs give the same result.  n_req == 0 is a no-op.
+ */
+smla_status sparse_mla_verify_tree(const float* target_probs, int64_t target_stride, const float* draft_probs,
+                                   int64_t draft_stride, const int32_t* tokens, const int32_t* parents,
+                                   const int32_t* cu_seqlens_q, const float* accept_u, const float* sample_u,
+                                   int32_t* keep, int32_t* out_tokens, int32_t* n_keep, int64_t n_req, int64_t n_tok,
+                                   int vocab, int max_keep, smla_stream_t stream);
+
+/*
+ * Commits what was kept of a step.  For request b with n_b = cu_seqlens_q[b + 1] - cu_seqlens_q[b] new tokens behind
+ * before = seqlens_k[b] - n_b cached ones, and m = n_keep[b], at most n_b and max_keep:
+ *   the row of position before + keep[b, i] goes to that of position before + i for i = 0 .. m - 1, in every layer;
+ *   seqlens[b] = before + m; the pages of table columns ceil(seqlens[b] / page_block) .. ceil(seqlens_k[b] /
+ *   page_block) - 1 go back to the free list.
+ * n_keep[b] < 0 ends the request: no row moves, seqlens[b] = 0 and all of its pages go back.
+ *   keep         [n_req, max_keep] int32, n_keep [n_req] int32: as sparse_mla_verify_tree writes them.  A request's
+ *                entries ascend and are below n_b; where they do not, its rows from before on are undefined.
+ *   seqlens_k    [n_req], cu_seqlens_q [n_req + 1], block_table [n_req, max_blocks]: as in the attention.  The table
+ *                is not changed: entries behind the new length are stale, and sparse_mla_plan_pages writes over them.
+ *                A row without a page is neither moved nor written.
+ *   kv_pool      [n_layers, pool_rows, d_qk] bf16, layers layer_stride elements apart (a multiple of 8, at least
+ *                pool_rows * d_qk), 16-byte aligned; n_layers 0: no rows are moved.  Rows from before on lie in pages of
+ *                the request's own.
+ *   free_pages   [n_free] int32 (written below free_start), or NULL: no page goes back.  sparse_mla_plan_pages hands out
+ *                from index free_start on; pages come back in front of it, request by request and column by
+ *                column, each to the index below the last.
+ *   free_start   [1] int32 or NULL for n_free (clamped to [0, n_free])
+ *   seqlens      [n_req] int32 (written)
+ *   counts       [3] int32 (written): tokens kept, the next free_start (0 without free_pages), pages for which there
+ *                was no room in front of free_start (they stay in the table only)
+ * counts + 1 is the next sparse_mla_plan_pages' free_start, seqlens its seqlens.  All other pointers 4-byte aligned; those
+ * of empty arrays may be NULL.  The stride of a single layer is not looked at.  SMLA_ERR_BAD_SHAPE when an output
+ * overlaps an input or another output.
+ */
+smla_status sparse_mla_commit_tree(const int32_t* keep, const int32_t* n_keep, int max_keep, const int32_t* cu_seqlens_q,
+                                   const int32_t* seqlens_k, const int32_t* block_table, int max_blocks, int page_block,
+                                   int64_t n_req, void* kv_pool, int n_layers, int64_t layer_stride, int64_t pool_rows,
+                                   int d_qk, int32_t* free_pages, int64_t n_free, const int32_t* free_start,
+                                   int32_t* seqlens, int32_t* counts, smla_stream_t stream);
 
 /* Static, human-readable description of a status code.  Never NULL. */
 const char* sparse_mla_status_string(smla_status status);

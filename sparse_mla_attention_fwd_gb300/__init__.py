@@ -26,6 +26,15 @@ A serving step on the paged cache that :func:`sparse_mla_fwd_paged` reads:
 
 gives the step's tokens their pages and rows, writes the rows, and attends to every cached key (the
 dense form, one token to whole prompts per request).
+
+A speculative step, where a request's new tokens are the nodes of a tree of drafts:
+
+    mask, positions = sparse_mla_plan_tree(parents, cu, seqlens_k, mask_words)
+    out, lse, max_logits = sparse_mla_tree_fwd_paged(q, kv_pool, block_table, cu, seqlens_k, mask)
+    keep, out_tokens, n_keep = sparse_mla_verify_tree(target_probs, tokens, parents, cu, accept_u, sample_u,
+                                                      max_keep, draft_probs)
+    seqlens, counts = sparse_mla_commit_tree(keep, n_keep, cu, seqlens_k, block_table, kv_pool,
+                                             free_pages=free_pages, free_start=free_start)
 """
 from __future__ import annotations
 
@@ -39,6 +48,7 @@ from .native_build import LIB_PATH, build as build_library
 __all__ = ["sparse_mla_fwd", "sparse_mla_fwd_paged", "sparse_mla_fwd_paged_splitkv_static", "sparse_mla_fwd_host",
            "row_shard", "sparse_mla_fwd_sharded", "auto_splits",
            "sparse_mla_bwd", "sparse_mla_plan_pages", "sparse_mla_append_kv", "sparse_mla_chunk_fwd_paged",
+           "sparse_mla_plan_tree", "sparse_mla_tree_fwd_paged", "sparse_mla_verify_tree", "sparse_mla_commit_tree",
            "sparse_mla_device_status",
            "sparse_mla_status_string", "SmlaError", "load_library", "build_library", "LIB_PATH"]
 
@@ -550,23 +560,11 @@ def sparse_mla_append_kv(c_kv, k_pe, slots, kv_pool, norm_weight=None, eps=1e-6,
     return kv_pool
 
 
-def sparse_mla_chunk_fwd_paged(q, kv_pool, block_table, cu_seqlens_q, seqlens_k, page_block=64, causal=True,
-                               attn_sink=None, sm_scale=None, d_v=512, out=None, lse=None, max_logits=None,
-                               workspace=None, stream=None):
-    """Dense attention of each request's new tokens over its paged cache.  q [n_tok, h, d_qk] bf16
-    (any h up to 1024), rows cu_seqlens_q[b] .. cu_seqlens_q[b+1]-1 being request b's new tokens;
-    kv_pool, block_table and page_block as for :func:`sparse_mla_fwd_paged`; seqlens_k [n_req] int32
-    counts the cached keys with the new tokens' own; causal: a token sees the positions up to its
-    own, else every key.  Returns (out [n_tok, h, d_v] bf16, lse [n_tok, h] fp32, max_logits [n_tok,
-    h] fp32); rows of no request are not written.  `workspace` (uint8, at least
-    sparse_mla_chunk_workspace_size bytes, 256-byte aligned) is allocated here when not given; calls
-    that may overlap must not share one."""
-    lib = load_library()
+def _dense_attention_args(q, kv_pool, block_table, cu_seqlens_q, seqlens_k, attn_sink, sm_scale, d_v, out, lse, max_logits,
+                          workspace, lib, dev):
+    """Checks of the dense attentions' tensors; returns the sizes, the outputs (allocated when not given), the scale and
+    the workspace."""
     bf16, i32, f32 = torch.bfloat16, torch.int32, torch.float32
-    dev = _dense(q, "q", bf16)
-    if stream is not None or torch.cuda.current_device() != dev.index:
-        return _on_device(sparse_mla_chunk_fwd_paged, dev, stream, q, kv_pool, block_table, cu_seqlens_q, seqlens_k, page_block,
-                          causal, attn_sink, sm_scale, d_v, out, lse, max_logits, workspace)
     _dense(kv_pool, "kv_pool", bf16, dev)
     _dense(block_table, "block_table", i32, dev)
     _dense(cu_seqlens_q, "cu_seqlens_q", i32, dev)
@@ -601,6 +599,27 @@ def sparse_mla_chunk_fwd_paged(q, kv_pool, block_table, cu_seqlens_q, seqlens_k,
     else:
         _dense(workspace, "workspace", torch.uint8, dev)
         ws_bytes = workspace.numel()
+    return n_tok, h_q, d_qk, pool_rows, n_req, max_blocks, out, lse, max_logits, sm_scale, workspace, ws_bytes
+
+
+def sparse_mla_chunk_fwd_paged(q, kv_pool, block_table, cu_seqlens_q, seqlens_k, page_block=64, causal=True,
+                               attn_sink=None, sm_scale=None, d_v=512, out=None, lse=None, max_logits=None,
+                               workspace=None, stream=None):
+    """Dense attention of each request's new tokens over its paged cache.  q [n_tok, h, d_qk] bf16
+    (any h up to 1024), rows cu_seqlens_q[b] .. cu_seqlens_q[b+1]-1 being request b's new tokens;
+    kv_pool, block_table and page_block as for :func:`sparse_mla_fwd_paged`; seqlens_k [n_req] int32
+    counts the cached keys with the new tokens' own; causal: a token sees the positions up to its
+    own, else every key.  Returns (out [n_tok, h, d_v] bf16, lse [n_tok, h] fp32, max_logits [n_tok,
+    h] fp32); rows of no request are not written.  `workspace` (uint8, at least
+    sparse_mla_chunk_workspace_size bytes, 256-byte aligned) is allocated here when not given; calls
+    that may overlap must not share one."""
+    lib = load_library()
+    dev = _dense(q, "q", torch.bfloat16)
+    if stream is not None or torch.cuda.current_device() != dev.index:
+        return _on_device(sparse_mla_chunk_fwd_paged, dev, stream, q, kv_pool, block_table, cu_seqlens_q, seqlens_k, page_block,
+                          causal, attn_sink, sm_scale, d_v, out, lse, max_logits, workspace)
+    n_tok, h_q, d_qk, pool_rows, n_req, max_blocks, out, lse, max_logits, sm_scale, workspace, ws_bytes = _dense_attention_args(
+        q, kv_pool, block_table, cu_seqlens_q, seqlens_k, attn_sink, sm_scale, d_v, out, lse, max_logits, workspace, lib, dev)
     rc = lib.sparse_mla_chunk_fwd_paged(
         q.data_ptr(), kv_pool.data_ptr(), pool_rows, block_table.data_ptr(), max_blocks, int(page_block),
         cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), n_req, 1 if causal else 0, _ptr(attn_sink), float(sm_scale), int(d_v),
@@ -609,6 +628,185 @@ def sparse_mla_chunk_fwd_paged(q, kv_pool, block_table, cu_seqlens_q, seqlens_k,
     if rc != 0:
         raise SmlaError(rc, "sparse_mla_chunk_fwd_paged")
     return out, lse, max_logits
+
+
+def sparse_mla_plan_tree(parents, cu_seqlens_q, seqlens_k, mask_words, tree_mask=None, positions=None, stream=None):
+    """Masks and positions of one speculative step's trees, on the device.  parents [n_tok] int32: each node's parent as an
+    index within its request, below its own (anything else: none); cu_seqlens_q [n_req + 1] and seqlens_k [n_req]
+    int32 as :func:`sparse_mla_plan_pages` returns them.  Returns tree_mask [n_tok, mask_words] int32 (bit j of word w of a
+    node's row: it sees node 32 w + j, that is itself and the nodes above it) and positions [n_tok] int32 (by depth; for
+    :func:`sparse_mla_append_kv`), allocated here when not given.  Rows of no request get 0 and -1."""
+    lib = load_library()
+    i32 = torch.int32
+    dev = _dense(parents, "parents", i32)
+    if stream is not None or torch.cuda.current_device() != dev.index:
+        return _on_device(sparse_mla_plan_tree, dev, stream, parents, cu_seqlens_q, seqlens_k, mask_words, tree_mask, positions)
+    _dense(cu_seqlens_q, "cu_seqlens_q", i32, dev)
+    _dense(seqlens_k, "seqlens_k", i32, dev)
+    n_tok, n_req, mask_words = parents.numel(), seqlens_k.numel(), int(mask_words)
+    if cu_seqlens_q.numel() != n_req + 1:
+        raise ValueError("cu_seqlens_q must have n_req + 1 entries")
+    if not 1 <= mask_words <= 1024:
+        raise ValueError("mask_words must be 1 to 1024")
+    if tree_mask is None:
+        tree_mask = _empty_strided((n_tok, mask_words), (mask_words, 1), i32)
+    else:
+        _dense(tree_mask, "tree_mask", i32, dev)
+        if tree_mask.shape != (n_tok, mask_words):
+            raise ValueError(f"tree_mask must be [{n_tok}, {mask_words}], got {list(tree_mask.shape)}")
+    positions = _int_output(positions, "positions", n_tok, dev)
+    rc = lib.sparse_mla_plan_tree(parents.data_ptr(), cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), tree_mask.data_ptr(),
+                                  positions.data_ptr(), n_req, n_tok, mask_words, _raw_stream(dev.index))
+    if rc != 0:
+        raise SmlaError(rc, "sparse_mla_plan_tree")
+    return tree_mask, positions
+
+
+def sparse_mla_tree_fwd_paged(q, kv_pool, block_table, cu_seqlens_q, seqlens_k, tree_mask, page_block=64, attn_sink=None,
+                              sm_scale=None, d_v=512, out=None, lse=None, max_logits=None, workspace=None, stream=None):
+    """:func:`sparse_mla_chunk_fwd_paged` for trees of drafted tokens: a token sees every key in front of its request's new
+    ones, and of the new ones those whose bit is set in its row of tree_mask [n_tok, words] int32 (see
+    :func:`sparse_mla_plan_tree`; any mask will do).  Everything else, workspace and returned values among it, is as
+    there."""
+    lib = load_library()
+    dev = _dense(q, "q", torch.bfloat16)
+    if stream is not None or torch.cuda.current_device() != dev.index:
+        return _on_device(sparse_mla_tree_fwd_paged, dev, stream, q, kv_pool, block_table, cu_seqlens_q, seqlens_k, tree_mask,
+                          page_block, attn_sink, sm_scale, d_v, out, lse, max_logits, workspace)
+    n_tok, h_q, d_qk, pool_rows, n_req, max_blocks, out, lse, max_logits, sm_scale, workspace, ws_bytes = _dense_attention_args(
+        q, kv_pool, block_table, cu_seqlens_q, seqlens_k, attn_sink, sm_scale, d_v, out, lse, max_logits, workspace, lib, dev)
+    _dense(tree_mask, "tree_mask", torch.int32, dev)
+    mask_shape = tree_mask.shape
+    if len(mask_shape) != 2 or mask_shape[0] != n_tok:
+        raise ValueError("tree_mask must be [n_tok, words]")
+    rc = lib.sparse_mla_tree_fwd_paged(
+        q.data_ptr(), kv_pool.data_ptr(), pool_rows, block_table.data_ptr(), max_blocks, int(page_block),
+        cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), n_req, tree_mask.data_ptr(), mask_shape[1], _ptr(attn_sink),
+        float(sm_scale), int(d_v), out.data_ptr(), lse.data_ptr(), max_logits.data_ptr(), n_tok, h_q, d_qk,
+        workspace.data_ptr(), ws_bytes, _raw_stream(dev.index))
+    if rc != 0:
+        raise SmlaError(rc, "sparse_mla_tree_fwd_paged")
+    return out, lse, max_logits
+
+
+def _probs(t, name, n_tok, vocab, dev):
+    """The row stride of an fp32 tensor [n_tok, vocab] whose last dimension is contiguous."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32:
+        raise TypeError(f"{name} must be a torch.float32 tensor")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.dim() != 2 or t.shape[0] != n_tok or (vocab is not None and t.shape[1] != vocab) or t.shape[1] < 1:
+        raise ValueError(f"{name} must be [{n_tok}, {'vocab' if vocab is None else vocab}], got {list(t.shape)}")
+    if t.stride(1) != 1 and t.numel() > 0 and t.shape[1] > 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    return t.stride(0)
+
+
+def sparse_mla_verify_tree(target_probs, tokens, parents, cu_seqlens_q, accept_u, sample_u, max_keep, draft_probs=None,
+                           keep=None, out_tokens=None, n_keep=None, stream=None):
+    """Which drafted tokens stand, and the token behind them.  target_probs [n_tok, vocab] fp32: the target's distribution
+    behind each node; tokens [n_tok] and parents [n_tok] int32 (node 0 of a request is its last known token);
+    cu_seqlens_q [n_req + 1] int32; accept_u [n_tok] and sample_u [n_req] fp32: random numbers in [0, 1).
+    draft_probs [n_tok, vocab] fp32: what a node's children were drawn from, independently; without it they count as
+    chosen outright.  Both may be strided over rows.  Returns int32 tensors (allocated here when not given): keep
+    [n_req, max_keep], node 0 and the nodes kept behind it (for :func:`sparse_mla_commit_tree`); out_tokens [n_req,
+    max_keep], their tokens but the first one's and the token drawn in the end; n_keep [n_req], how many.  The tokens
+    follow the target's distribution.  See the C header for the exact rules."""
+    lib = load_library()
+    i32, f32 = torch.int32, torch.float32
+    dev = _dense(tokens, "tokens", i32)
+    if stream is not None or torch.cuda.current_device() != dev.index:
+        return _on_device(sparse_mla_verify_tree, dev, stream, target_probs, tokens, parents, cu_seqlens_q, accept_u, sample_u,
+                          max_keep, draft_probs, keep, out_tokens, n_keep)
+    _dense(parents, "parents", i32, dev)
+    _dense(cu_seqlens_q, "cu_seqlens_q", i32, dev)
+    _dense(accept_u, "accept_u", f32, dev)
+    _dense(sample_u, "sample_u", f32, dev)
+    n_tok, n_req, max_keep = tokens.numel(), sample_u.numel(), int(max_keep)
+    if parents.numel() != n_tok or accept_u.numel() != n_tok:
+        raise ValueError("parents and accept_u must have one entry per token")
+    if cu_seqlens_q.numel() != n_req + 1:
+        raise ValueError("cu_seqlens_q must have one entry more than sample_u")
+    if max_keep < 1:
+        raise ValueError("max_keep must be at least 1")
+    t_stride = _probs(target_probs, "target_probs", n_tok, None, dev)
+    vocab = target_probs.shape[1]
+    d_stride = 0 if draft_probs is None else _probs(draft_probs, "draft_probs", n_tok, vocab, dev)
+    if keep is None:
+        keep = _empty_strided((n_req, max_keep), (max_keep, 1), i32)
+    if out_tokens is None:
+        out_tokens = _empty_strided((n_req, max_keep), (max_keep, 1), i32)
+    for t, name in ((keep, "keep"), (out_tokens, "out_tokens")):
+        _dense(t, name, i32, dev)
+        if t.shape != (n_req, max_keep):
+            raise ValueError(f"{name} must be [{n_req}, {max_keep}], got {list(t.shape)}")
+    n_keep = _int_output(n_keep, "n_keep", n_req, dev)
+    rc = lib.sparse_mla_verify_tree(
+        target_probs.data_ptr(), t_stride, _ptr(draft_probs), d_stride, tokens.data_ptr(), parents.data_ptr(),
+        cu_seqlens_q.data_ptr(), accept_u.data_ptr(), sample_u.data_ptr(), keep.data_ptr(), out_tokens.data_ptr(),
+        n_keep.data_ptr(), n_req, n_tok, vocab, max_keep, _raw_stream(dev.index))
+    if rc != 0:
+        raise SmlaError(rc, "sparse_mla_verify_tree")
+    return keep, out_tokens, n_keep
+
+
+def sparse_mla_commit_tree(keep, n_keep, cu_seqlens_q, seqlens_k, block_table, kv_pool, page_block=64, free_pages=None,
+                           free_start=None, seqlens=None, counts=None, stream=None):
+    """Commits a speculative step: of each request's new tokens the rows keep[b, :n_keep[b]] (int32, ascending, as
+    :func:`sparse_mla_verify_tree` returns them) are moved together behind the cached ones, in kv_pool [rows, 1, d_qk] or
+    [layers, rows, 1, d_qk] bf16 (every layer; layers may be strided; None: no rows are moved), and the pages behind the
+    new lengths go back into free_pages [n_free] int32 in front of index free_start [1] (int32; None: n_free).  A
+    request with n_keep[b] < 0 is done: its length becomes 0 and all its pages go back.  Returns int32 tensors (allocated
+    here when not given): seqlens [n_req], and counts [3] = tokens kept, next free_start, pages without room;
+    both go into the next :func:`sparse_mla_plan_pages`.  block_table is not changed.  With a tensor per layer, call once
+    per layer and give free_pages in one of the calls."""
+    lib = load_library()
+    i32 = torch.int32
+    dev = _dense(keep, "keep", i32)
+    if stream is not None or torch.cuda.current_device() != dev.index:
+        return _on_device(sparse_mla_commit_tree, dev, stream, keep, n_keep, cu_seqlens_q, seqlens_k, block_table, kv_pool,
+                          page_block, free_pages, free_start, seqlens, counts)
+    _dense(n_keep, "n_keep", i32, dev)
+    _dense(cu_seqlens_q, "cu_seqlens_q", i32, dev)
+    _dense(seqlens_k, "seqlens_k", i32, dev)
+    _dense(block_table, "block_table", i32, dev)
+    n_req, keep_shape, table_shape = seqlens_k.numel(), keep.shape, block_table.shape
+    if len(keep_shape) != 2 or keep_shape[0] != n_req or keep_shape[1] < 1 or n_keep.numel() != n_req:
+        raise ValueError("keep must be [n_req, max_keep] and n_keep have n_req entries")
+    if cu_seqlens_q.numel() != n_req + 1:
+        raise ValueError("cu_seqlens_q must have n_req + 1 entries")
+    if len(table_shape) != 2 or table_shape[0] != n_req:
+        raise ValueError("block_table must be [n_req, max_blocks]")
+    layers = layer_stride = pool_rows = d_qk = 0
+    if kv_pool is not None:
+        if not isinstance(kv_pool, torch.Tensor) or kv_pool.dtype is not torch.bfloat16:
+            raise TypeError("kv_pool must be a torch.bfloat16 tensor")
+        if kv_pool.device != dev:
+            raise ValueError(f"kv_pool is on {kv_pool.device}, expected {dev}")
+        shape = kv_pool.shape
+        if len(shape) not in (3, 4) or shape[-2] != 1 or shape[-1] not in (512, 576):
+            raise ValueError("kv_pool must be [rows, 1, d_qk] or [layers, rows, 1, d_qk] with d_qk 512 or 576")
+        layers, pool_rows, d_qk = shape[0] if len(shape) == 4 else 1, shape[-3], shape[-1]
+        layer_stride = kv_pool.stride(0) if len(shape) == 4 else 0
+        strides = kv_pool.stride()
+        if kv_pool.numel() > 0 and (strides[-1] != 1 or (pool_rows > 1 and strides[-3] != d_qk)):
+            raise ValueError("kv_pool must be contiguous within a layer")
+    n_free = 0
+    if free_pages is not None:
+        _dense(free_pages, "free_pages", i32, dev)
+        n_free = free_pages.numel()
+    if free_start is not None:
+        _dense(free_start, "free_start", i32, dev)
+        if free_start.numel() != 1:
+            raise ValueError("free_start must have one entry")
+    seqlens, counts = _int_output(seqlens, "seqlens", n_req, dev), _int_output(counts, "counts", 3, dev)
+    rc = lib.sparse_mla_commit_tree(
+        keep.data_ptr(), n_keep.data_ptr(), keep_shape[1], cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), block_table.data_ptr(),
+        table_shape[1], int(page_block), n_req, _ptr(kv_pool), layers, layer_stride, pool_rows, d_qk, _ptr(free_pages), n_free,
+        _ptr(free_start), seqlens.data_ptr(), counts.data_ptr(), _raw_stream(dev.index))
+    if rc != 0:
+        raise SmlaError(rc, "sparse_mla_commit_tree")
+    return seqlens, counts
 
 
 def sparse_mla_device_status(reset=False) -> int:

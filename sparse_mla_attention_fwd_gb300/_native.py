@@ -20,7 +20,8 @@ EXPORTED = ("sparse_mla_fwd", "sparse_mla_fwd_paged", "sparse_mla_splitkv_worksp
             "sparse_mla_fwd_host", "sparse_mla_selftest_wait_timeout", "sparse_mla_device_status",
             "sparse_mla_status_string", "sparse_mla_abi_version", "sparse_mla_bwd", "sparse_mla_plan_pages",
             "sparse_mla_append_kv", "sparse_mla_append_kv_counted", "sparse_mla_chunk_workspace_size",
-            "sparse_mla_chunk_fwd_paged", "sparse_mla_chunk_device_status", "sparse_mla_chunk_selftest_wait_timeout")
+            "sparse_mla_chunk_fwd_paged", "sparse_mla_chunk_device_status", "sparse_mla_chunk_selftest_wait_timeout",
+            "sparse_mla_plan_tree", "sparse_mla_tree_fwd_paged", "sparse_mla_verify_tree", "sparse_mla_commit_tree")
 
 _lock = threading.Lock()
 _lib = None
@@ -94,6 +95,15 @@ def load_library(path: str | None = None):
         lib.sparse_mla_chunk_device_status.argtypes = [I32]
         lib.sparse_mla_chunk_selftest_wait_timeout.restype = I32
         lib.sparse_mla_chunk_selftest_wait_timeout.argtypes = [ctypes.c_uint64, P]
+        lib.sparse_mla_plan_tree.restype = I32
+        lib.sparse_mla_plan_tree.argtypes = [P, P, P, P, P, I64, I64, I32, P]
+        lib.sparse_mla_tree_fwd_paged.restype = I32
+        lib.sparse_mla_tree_fwd_paged.argtypes = [P, P, I64, P, I32, I32, P, P, I64, P, I32, P, F32, I32, P, P, P, I64,
+                                                  I32, I32, P, SZ, P]
+        lib.sparse_mla_verify_tree.restype = I32
+        lib.sparse_mla_verify_tree.argtypes = [P, I64, P, I64, P, P, P, P, P, P, P, P, I64, I64, I32, I32, P]
+        lib.sparse_mla_commit_tree.restype = I32
+        lib.sparse_mla_commit_tree.argtypes = [P, P, I32, P, P, P, I32, I32, I64, P, I32, I64, I64, I32, P, I64, P, P, P, P]
         _lib = lib
         return lib
 

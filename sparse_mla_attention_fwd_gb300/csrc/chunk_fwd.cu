@@ -116,6 +116,8 @@ struct ChunkParams {
   int pool_end;             // first row behind the pool
   int tokens_per_tile, groups;   // 128 / h_q and 1, or 1 and the 128-head groups of a token
   int row_cap;
+  const int32_t* tree_mask;      // [n_tok, mask_words], the tree form alone
+  int mask_words;
 };
 
 // ------------------------------------------------------------------------ lengths and the axis
@@ -164,7 +166,7 @@ struct __align__(16) BlockDesc {
   uint32_t flags;
   int32_t key0;          // position of the block's first key
   int32_t q_row, n_rows; // tile: first (token, head) row, rows
-  int32_t pos0;          // position of the tile's first token
+  int32_t pos0;          // position of the tile's first token; TREE: of its request's first new one
   int32_t key_end;       // keys of the tile
   int32_t part;          // workspace slot, or -1: the whole tile is done here
 };
@@ -264,7 +266,16 @@ __device__ __forceinline__ int64_t pair_scan(int64_t v, int64_t* warp_sum) {   /
   return v;
 }
 
-template <int D_QK>
+// Bits [at, at + 32) of a row of words, bits outside it 0.
+__device__ __forceinline__ uint32_t bits_at(const int32_t* words, int n_words, int64_t at) {
+  const int64_t w = at >> 5;
+  const uint32_t lo = w >= 0 && w < n_words ? __ldg(words + w) : 0u;
+  const uint32_t hi = w + 1 >= 0 && w + 1 < n_words ? __ldg(words + w + 1) : 0u;
+  return __funnelshift_r(lo, hi, static_cast<uint32_t>(at) & 31u);
+}
+
+// TREE: a token sees every key in front of its request's new ones, and of those the ones in its mask.
+template <int D_QK, bool TREE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     chunk_fwd_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap half_map,
                      const __grid_constant__ CUtensorMap box_map, const __grid_constant__ CUtensorMap group_map,
@@ -386,15 +397,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const uint32_t key_mask = d.mask[half];
       const int key0 = d.key0 + 32 * half;
       if (flags & kFirst) {
-        const int64_t seen = p.causal ? static_cast<int64_t>(d.pos0) + (p.groups == 1 ? row / p.h_q : 0) + 1 : d.key_end;
+        const int64_t seen = TREE ? d.pos0 : p.causal ? static_cast<int64_t>(d.pos0) + (p.groups == 1 ? row / p.h_q : 0) + 1 : d.key_end;
         limit = row < n_rows ? static_cast<int>(min(max(seen, static_cast<int64_t>(0)), static_cast<int64_t>(d.key_end))) : 0;
         m = top = -INFINITY;
         l = 0.f;
       }
+      const int first_new = d.pos0;                  // TREE: position of the request's first new token
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&c.ring_empty[b % kRing]));
       const int n_seen = limit - key0;
-      const uint32_t mask = n_seen >= 32 ? key_mask : n_seen <= 0 ? 0u : key_mask & ((1u << n_seen) - 1u);
+      uint32_t mask = n_seen >= 32 ? key_mask : n_seen <= 0 ? 0u : key_mask & ((1u << n_seen) - 1u);
+      if constexpr (TREE) {
+        if (n_seen < 32 && row < n_rows)
+          mask |= key_mask & bits_at(p.tree_mask + static_cast<int64_t>(static_cast<uint32_t>(q_row + row) / static_cast<uint32_t>(p.h_q)) * p.mask_words,
+                                     p.mask_words, static_cast<int64_t>(key0) - first_new);
+      }
 
       wait_on(&c.s_full[g], (b / kGens) & 1, abort);
       __syncwarp();
@@ -701,7 +718,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
               d.key0 = static_cast<int32_t>(kKeys * j);
               d.q_row = static_cast<int32_t>(q_row);
               d.n_rows = n_rows;
-              d.pos0 = static_cast<int32_t>(before + tok);
+              d.pos0 = static_cast<int32_t>(TREE ? before : before + tok);
               d.key_end = static_cast<int32_t>(key_end);
               d.part = part;
             }
@@ -1041,18 +1058,21 @@ int device_sms() {
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 0;
   if ((n = sms[dev].load(std::memory_order_acquire)) > 0) return n;
-  if (cudaFuncSetAttribute(chunk_fwd_kernel<512>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<512>::kBytes) != cudaSuccess ||
-      cudaFuncSetAttribute(chunk_fwd_kernel<576>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<576>::kBytes) != cudaSuccess ||
+  constexpr auto kLimit = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  if (cudaFuncSetAttribute(chunk_fwd_kernel<512, false>, kLimit, Smem<512>::kBytes) != cudaSuccess ||
+      cudaFuncSetAttribute(chunk_fwd_kernel<576, false>, kLimit, Smem<576>::kBytes) != cudaSuccess ||
+      cudaFuncSetAttribute(chunk_fwd_kernel<512, true>, kLimit, Smem<512>::kBytes) != cudaSuccess ||
+      cudaFuncSetAttribute(chunk_fwd_kernel<576, true>, kLimit, Smem<576>::kBytes) != cudaSuccess ||
       cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return 0;
   sms[dev].store(n, std::memory_order_release);
   return n;
 }
 
-template <int D_QK>
+template <int D_QK, bool TREE>
 smla_status launch(const CUtensorMap& qm, const CUtensorMap& hm, const CUtensorMap& bm, const CUtensorMap& gm,
                    const CUtensorMap& rm, const ChunkParams& p, int pairs, cudaStream_t stream) {
-  chunk_fwd_kernel<D_QK><<<2 * pairs, kPairThreads, Smem<D_QK>::kBytes, stream>>>(qm, hm, bm, gm, rm, p);
+  chunk_fwd_kernel<D_QK, TREE><<<2 * pairs, kPairThreads, Smem<D_QK>::kBytes, stream>>>(qm, hm, bm, gm, rm, p);
   if (cudaGetLastError() != cudaSuccess) return SMLA_ERR_LAUNCH;
   // the joining kernel's CTAs come up while the first one still runs, and wait for its end
   cudaLaunchAttribute early{};
@@ -1067,36 +1087,26 @@ smla_status launch(const CUtensorMap& qm, const CUtensorMap& hm, const CUtensorM
   return cudaLaunchKernelEx(&cfg, chunk_join_kernel, p) == cudaSuccess ? SMLA_OK : SMLA_ERR_LAUNCH;
 }
 
-}  // namespace
-}  // namespace smla
-
-using namespace smla;
-
-extern "C" {
-
-size_t sparse_mla_chunk_workspace_size(int64_t n_tok, int h_q) {
-  if (n_tok <= 0 || h_q < 1 || h_q > 1024 || n_tok > INT32_MAX / h_q) return 0;
-  return workspace_of(n_tok, h_q).bytes;
-}
-
-smla_status sparse_mla_chunk_fwd_paged(const void* q, const void* kv_pool, int64_t pool_rows,
-                                       const int32_t* block_table, int max_blocks, int page_block,
-                                       const int32_t* cu_seqlens_q, const int32_t* seqlens_k, int64_t n_req, int causal,
-                                       const float* attn_sink, float sm_scale, int d_v, void* out, float* lse,
-                                       float* max_logits, int64_t n_tok, int h_q, int d_qk, void* workspace,
-                                       size_t workspace_bytes, smla_stream_t stream) {
+template <bool TREE>
+smla_status dense_fwd(const void* q, const void* kv_pool, int64_t pool_rows, const int32_t* block_table, int max_blocks,
+                      int page_block, const int32_t* cu_seqlens_q, const int32_t* seqlens_k, int64_t n_req, int causal,
+                      const int32_t* tree_mask, int mask_words, const float* attn_sink, float sm_scale, int d_v, void* out,
+                      float* lse, float* max_logits, int64_t n_tok, int h_q, int d_qk, void* workspace,
+                      size_t workspace_bytes, smla_stream_t stream) {
   if (n_tok < 0 || n_req < 0 || n_req > INT32_MAX || h_q < 1 || h_q > 1024 || (d_qk != 512 && d_qk != 576) ||
-      d_v != kDv || !(sm_scale > 0.f) || !std::isfinite(sm_scale) || n_tok > INT32_MAX / h_q)
+      d_v != kDv || !(sm_scale > 0.f) || !std::isfinite(sm_scale) || n_tok > INT32_MAX / h_q ||
+      (TREE && (mask_words < 1 || mask_words > 1024)))
     return SMLA_ERR_BAD_SHAPE;
   if (n_tok == 0 || n_req == 0) return SMLA_OK;
   if (pool_rows < 1 || pool_rows > INT32_MAX || max_blocks < 1 || page_block < 1 ||
       static_cast<int64_t>(max_blocks) * page_block > INT32_MAX)
     return SMLA_ERR_BAD_SHAPE;
-  if (!q || !kv_pool || !block_table || !cu_seqlens_q || !seqlens_k || !out || !lse || !max_logits)
+  if (!q || !kv_pool || !block_table || !cu_seqlens_q || !seqlens_k || !out || !lse || !max_logits ||
+      (TREE && !tree_mask))
     return SMLA_ERR_NULL_PTR;
   if (!aligned_to(q, 16) || !aligned_to(kv_pool, 16) || !aligned_to(out, 16) || !aligned_to(lse, 4) ||
       !aligned_to(max_logits, 4) || !aligned_to(block_table, 4) || !aligned_to(cu_seqlens_q, 4) ||
-      !aligned_to(seqlens_k, 4) || !aligned_to(attn_sink, 4))
+      !aligned_to(seqlens_k, 4) || !aligned_to(attn_sink, 4) || !aligned_to(tree_mask, 4))
     return SMLA_ERR_MISALIGNED;
   const Workspace ws = workspace_of(n_tok, h_q);
   if (!workspace || workspace_bytes < ws.bytes) return SMLA_ERR_WORKSPACE;
@@ -1105,7 +1115,7 @@ smla_status sparse_mla_chunk_fwd_paged(const void* q, const void* kv_pool, int64
   const size_t rows = static_cast<size_t>(n_tok) * h_q, reqs = static_cast<size_t>(n_req) * 4;
   const Span in[] = {{q, rows * d_qk * 2}, {kv_pool, static_cast<size_t>(pool_rows) * d_qk * 2},
                      {block_table, reqs * max_blocks}, {cu_seqlens_q, reqs + 4}, {seqlens_k, reqs},
-                     {attn_sink, static_cast<size_t>(h_q) * 4}};
+                     {attn_sink, static_cast<size_t>(h_q) * 4}, {tree_mask, static_cast<size_t>(n_tok) * mask_words * 4}};
   const Span written[] = {{out, rows * kDv * 2}, {lse, rows * 4}, {max_logits, rows * 4}, {workspace, ws.bytes}};
   if (any_overlap(in, written)) return SMLA_ERR_BAD_SHAPE;
   const int sms = device_sms();
@@ -1129,6 +1139,8 @@ smla_status sparse_mla_chunk_fwd_paged(const void* q, const void* kv_pool, int64
   p.max_blocks = max_blocks;
   p.page_block = page_block;
   p.causal = causal != 0;
+  p.tree_mask = tree_mask;
+  p.mask_words = mask_words;
   // Tiled loads take rows of one page, in groups of eight (the 128-byte swizzle's pattern): three and one for a
   // CTA's part of a block at 32 rows, against 104 gathers of four rows where the page size is not a multiple of 8.
   // 256 tokens over 1024-4096 keys: pages of 64 and 32 163-170 us, 16 185 us, 8 and 24 235 us, 100 473 us, 20 492 us, 1
@@ -1145,7 +1157,41 @@ smla_status sparse_mla_chunk_fwd_paged(const void* q, const void* kv_pool, int64
     return SMLA_ERR_TENSOR_MAP;
   const int pairs = sms / 2 < kMaxPairs ? sms / 2 : kMaxPairs;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return d_qk == 512 ? launch<512>(qm, hm, bm, gm, rm, p, pairs, s) : launch<576>(qm, hm, bm, gm, rm, p, pairs, s);
+  return d_qk == 512 ? launch<512, TREE>(qm, hm, bm, gm, rm, p, pairs, s) : launch<576, TREE>(qm, hm, bm, gm, rm, p, pairs, s);
+}
+
+}  // namespace
+}  // namespace smla
+
+using namespace smla;
+
+extern "C" {
+
+size_t sparse_mla_chunk_workspace_size(int64_t n_tok, int h_q) {
+  if (n_tok <= 0 || h_q < 1 || h_q > 1024 || n_tok > INT32_MAX / h_q) return 0;
+  return workspace_of(n_tok, h_q).bytes;
+}
+
+smla_status sparse_mla_chunk_fwd_paged(const void* q, const void* kv_pool, int64_t pool_rows,
+                                       const int32_t* block_table, int max_blocks, int page_block,
+                                       const int32_t* cu_seqlens_q, const int32_t* seqlens_k, int64_t n_req, int causal,
+                                       const float* attn_sink, float sm_scale, int d_v, void* out, float* lse,
+                                       float* max_logits, int64_t n_tok, int h_q, int d_qk, void* workspace,
+                                       size_t workspace_bytes, smla_stream_t stream) {
+  return dense_fwd<false>(q, kv_pool, pool_rows, block_table, max_blocks, page_block, cu_seqlens_q, seqlens_k, n_req, causal,
+                          nullptr, 0, attn_sink, sm_scale, d_v, out, lse, max_logits, n_tok, h_q, d_qk, workspace,
+                          workspace_bytes, stream);
+}
+
+smla_status sparse_mla_tree_fwd_paged(const void* q, const void* kv_pool, int64_t pool_rows,
+                                      const int32_t* block_table, int max_blocks, int page_block,
+                                      const int32_t* cu_seqlens_q, const int32_t* seqlens_k, int64_t n_req,
+                                      const int32_t* tree_mask, int mask_words, const float* attn_sink, float sm_scale,
+                                      int d_v, void* out, float* lse, float* max_logits, int64_t n_tok, int h_q, int d_qk,
+                                      void* workspace, size_t workspace_bytes, smla_stream_t stream) {
+  return dense_fwd<true>(q, kv_pool, pool_rows, block_table, max_blocks, page_block, cu_seqlens_q, seqlens_k, n_req, 0,
+                         tree_mask, mask_words, attn_sink, sm_scale, d_v, out, lse, max_logits, n_tok, h_q, d_qk, workspace,
+                         workspace_bytes, stream);
 }
 
 smla_status sparse_mla_chunk_selftest_wait_timeout(uint64_t limit_ns, smla_stream_t stream) {

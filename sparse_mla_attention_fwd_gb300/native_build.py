@@ -14,7 +14,8 @@ PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
 LIB_NAME = "libsparse_mla_gb300.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
-SOURCES = [os.path.join(PKG_DIR, "csrc", f) for f in ("sparse_mla_fwd.cu", "chunk_fwd.cu", "paged_cache.cu")]
+SOURCES = [os.path.join(PKG_DIR, "csrc", f) for f in ("sparse_mla_fwd.cu", "chunk_fwd.cu", "paged_cache.cu",
+                                                  "tree_step.cu")]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
