@@ -430,8 +430,8 @@ smla_status sparse_mla_tree_fwd_paged(const void* q, const void* kv_pool, int64_
  * When no child is left, or max_keep nodes are kept, the request's last token is drawn from the current r: the first v
  * with r(0) + .. + r(v) > sample_u[b] * sum r (the last v with r(v) > 0 where rounding leaves none; with r all zero,
  * p's; -1 when p has no positive value).  The tokens kept and drawn follow the target's distribution, whatever the
- * drafts.  Sums of r, Z and the comparisons are in 64 bits (in effect: products of two fp32 numbers are exact).
- *   target_probs [n_tok, vocab] fp32, row stride target_stride elements (>= vocab); rows sum to 1; NaN and negative
+ * drafts.  Products, sums of r, Z and the comparisons hold 46 bits and more, in an order that depends on the sizes alone.
+ *   target_probs [n_tok, vocab] fp32, vocab 1 .. 2^30, row stride target_stride elements (>= vocab); rows sum to 1; NaN and negative
  *                values count as 0
  *   draft_probs  [n_tok, vocab] fp32, row stride draft_stride, or NULL; row t is what node t's children were drawn
  *                from (rows of nodes without children are not read); values >= 0

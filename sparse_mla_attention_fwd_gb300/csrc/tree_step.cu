@@ -9,6 +9,7 @@
 
 #include "../../include/sparse_mla.h"
 #include "host_util.cuh"
+#include "pair_ptx.cuh"
 
 namespace smla {
 namespace {
@@ -107,12 +108,28 @@ __global__ void __launch_bounds__(32 * kPlanWarps) plan_tree_kernel(const TreePl
 // with r(v_0) + .. + r(v) > u sum r.
 //
 // Values near that border decide which token comes out, so sums must not depend on how the row is cut: r is rounded
-// to fp32 once (C too: 2^-24 of q, far below what q itself is known to), and sums of r are held in two floats per lane
-// (the rounding error of each addition is added up beside the sum) and in 64 bits from there on.
-constexpr int kVerifyThreads = 512;
+// to fp32 once (C too: 2^-24 of q, far below what q itself is known to), and every sum of r, Z and the comparisons with them are
+// held in two floats, the second one for what the additions to the first have lost: 48 bits.  (64-bit additions run at two a
+// clock and SM; the walk and the scans in 64 bits, with one more level of the search, took 3 us more.)
+//
+// A cluster of CTAs takes a request, each a contiguous part of the vocabulary, cut into tiles whose sums stay in shared
+// memory.  All CTAs walk the tree alike; they exchange their sums only (one cluster barrier a pass).  The last token's place
+// is narrowed down from the CTAs' sums to a tile's and to four values a thread, so a row is read once a pass.
+//
+// What bounds it.  Large batches: DRAM.  256 chains of up to six nodes over 128000 tokens, 236 MB: 45 us, of which 37 us are
+// the rows (6.4 TB/s; 6.7 TB/s by the difference of two vocabularies) and 8 us the chain of latencies in front (sums of nodes,
+// nodes, their probabilities, the walk) and behind (exchange, search).  Small ones: that chain, 5.7 us for a request of one
+// node and 32000 tokens, and 3 us for each further pass (32 trees with up to five rejections at a node over 100003 tokens:
+// 21 us).  One CTA a request instead of a cluster: 1 chain 25 us, 32 trees 203 us.  Two steps of loads under way per warp;
+// three and four, copies through shared memory (cp.async, 4 bytes) and CTAs of 512 or 1024 threads were no faster.
+constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
+constexpr int kMaxCluster = 8;
+constexpr int kMaxVocab = 1 << 30;
 constexpr int kMaxNodes = 1024;       // of a request; further ones are not tested
-constexpr int kScanLen = 256;         // a range that one warp searches
+constexpr int kWindow = 256;          // nodes in shared memory at a time
+constexpr int kMaxTiles = 256;        // of a CTA
+constexpr int kTile = 4 * kVerifyThreads;   // values of a tile at most, where kMaxTiles of them are enough
 
 struct VerifyParams {
   const float* target;
@@ -127,6 +144,7 @@ struct VerifyParams {
   int32_t* n_keep;
   int64_t target_stride, draft_stride, n_req, n_tok;
   int vocab, max_keep;
+  int each, tile;            // values of a CTA, of a tile
 };
 
 // What is left of the current node's row.
@@ -138,7 +156,7 @@ struct Residual {
   int n_gone;
 };
 
-__device__ __forceinline__ float left_of(const Residual& r, int64_t v) {
+__device__ __forceinline__ float left_of(const Residual& r, int v) {
   const float x = __ldg(r.p + v);
   if (r.q && r.c > 0.f) return fmaxf(fmaf(-r.c, __ldg(r.q + v), x), 0.f);
   for (int i = 0; i < r.n_gone; ++i)
@@ -146,110 +164,210 @@ __device__ __forceinline__ float left_of(const Residual& r, int64_t v) {
   return fmaxf(x, 0.f);
 }
 
-// Sum of r over [v0, v1), in every lane.
-__device__ __forceinline__ double sum_of(const Residual& r, int64_t v0, int64_t v1) {
-  float hi = 0.f, lo = 0.f;
-  for (int64_t v = v0 + (threadIdx.x & 31); v < v1; v += 32) {
-    const float x = left_of(r, v);
+// A sum in two floats: hi, and in lo what the additions to hi have lost.  64-bit additions run at 2 a clock and SM here.
+struct __align__(8) Sum {
+  float hi, lo;
+  __device__ __forceinline__ void add(float x) {
     const float s = hi + x, t = s - hi;
-    lo += (hi - (s - t)) + (x - t);     // what the addition lost
+    lo += (hi - (s - t)) + (x - t);
     hi = s;
   }
-  double sum = static_cast<double>(hi) + lo;
+  __device__ __forceinline__ void add(const Sum& x) {
+    add(x.hi);
+    lo += x.lo;
+  }
+  // Whether it is above x.  (The difference of the high parts is exact where they are close.)
+  __device__ __forceinline__ bool above(const Sum& x) const { return (hi - x.hi) + (lo - x.lo) > 0.f; }
+  __device__ __forceinline__ bool positive() const { return hi + lo > 0.f; }
+};
+// Over the warp: the same in every lane, and the sum up to and with a lane's own.
+__device__ __forceinline__ void add_lanes(Sum& v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-  return sum;
+  for (int o = 16; o > 0; o >>= 1) {
+    const float hi = __shfl_xor_sync(kAll, v.hi, o), lo = __shfl_xor_sync(kAll, v.lo, o);
+    const float small = fminf(v.hi, hi);
+    v = {fmaxf(v.hi, hi), v.lo + lo};      // one order in both lanes
+    v.add(small);
+  }
+}
+__device__ __forceinline__ Sum upto_lane(Sum v) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const Sum x{__shfl_up_sync(kAll, v.hi, o), __shfl_up_sync(kAll, v.lo, o)};
+    if ((threadIdx.x & 31) >= o) v.add(x);
+  }
+  return v;
+}
+__device__ __forceinline__ Sum of_lane(const Sum& v, int lane) {
+  return {__shfl_sync(kAll, v.hi, lane), __shfl_sync(kAll, v.lo, lane)};
 }
 
-struct VerifyShared {
-  int32_t parent[kMaxNodes], token[kMaxNodes], gone[kMaxNodes];
-  float u[kMaxNodes], px[kMaxNodes], qx[kMaxNodes];
-  double sums[kVerifyWarps];
-  double z;
-  float c;
-  int cur, kept, next, n_gone, ask;
-  int64_t v0, v1;
-  double before;
+// Four values a lane of r's row (and of q's), of the 128 from v on; 0 outside [0, end).
+template <bool DRAFT, bool WIDE>
+struct Step {
+  float p[4], q[DRAFT ? 4 : 1];
+  __device__ __forceinline__ void load(const Residual& r, int v, int end) {
+    const int at = v + (WIDE ? 4 : 1) * (threadIdx.x & 31);
+    if (WIDE && at >= 0 && at + 4 <= end) {
+      const float4 a = __ldg(reinterpret_cast<const float4*>(r.p + at));
+      p[0] = a.x, p[1] = a.y, p[2] = a.z, p[3] = a.w;
+      if (DRAFT) {
+        const float4 d = __ldg(reinterpret_cast<const float4*>(r.q + at));
+        q[0] = d.x, q[DRAFT ? 1 : 0] = d.y, q[DRAFT ? 2 : 0] = d.z, q[DRAFT ? 3 : 0] = d.w;
+      }
+      return;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int x = at + (WIDE ? 1 : 32) * u;
+      const bool in = x >= 0 && x < end;
+      p[u] = in ? __ldg(r.p + x) : 0.f;
+      if (DRAFT) q[u] = in ? __ldg(r.q + x) : 0.f;
+    }
+  }
 };
 
-// The first of n sums at which base + their running sum passes `target`, else the last that is above 0, else -1;
-// `before` becomes base + the sums in front of it.  One warp.
-__device__ __forceinline__ int crossing(const double* sums, int n, double target, double& before) {
+// Sums of r over the tiles of [v0, v1), tile values each (a multiple of 256), into sums[0], sums[1], ..; a warp.  Two steps' loads
+// are under way, and four sums a lane are added to in turn.
+template <bool DRAFT, bool WIDE>
+__device__ __forceinline__ void tile_sums(const Residual& r, int v0, int v1, int tile, Sum* sums) {
   const int lane = threadIdx.x & 31;
-  double run = before;
-  int last = -1;
-  double at_last = run;
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    const double x = i0 + lane < n ? sums[i0 + lane] : 0.0;
-    double end = x;
+  Step<DRAFT, WIDE> step[2];
+  step[0].load(r, v0, v1);
+  step[1].load(r, v0 + 128, v1);
+  for (int a = v0; a < v1; a += tile, ++sums) {
+    const int end = min(a + tile, v1);
+    Sum part[4] = {};
+    uint32_t skip = 0;                 // this lane's values of 1024 that are gone: bit 4 step + u
+    for (int v = a; v < end; v += 256) {
+      if (!DRAFT && ((v - a) & 1023) == 0) {
+        skip = 0;
+        for (int i = 0; i < r.n_gone; ++i) {
+          const uint32_t d = static_cast<uint32_t>(r.gone[i] - v);
+          if (d < 1024u && (WIDE ? (d >> 2) & 31 : d & 31) == lane) skip |= 1u << (((d >> 7) << 2) + (WIDE ? d & 3 : (d >> 5) & 3));
+        }
+      }
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double u = __shfl_up_sync(kAll, end, o);
-      if (lane >= o) end += u;
+      for (int k = 0; k < 2; ++k) {
+        float x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          x[u] = fmaxf(DRAFT ? fmaf(-r.c, step[k].q[DRAFT ? u : 0], step[k].p[u]) : step[k].p[u], 0.f);
+          if (!DRAFT && (skip >> u & 1)) x[u] = 0.f;
+        }
+        skip >>= 4;
+        step[k].load(r, v + 256 + 128 * k, v1);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) part[u].add(x[u]);
+      }
     }
-    const uint32_t hit = __ballot_sync(kAll, i0 + lane < n && x > 0.0 && run + end > target);
-    const uint32_t some = __ballot_sync(kAll, x > 0.0);
+#pragma unroll
+    for (int u = 1; u < 4; ++u) part[0].add(part[u]);
+    add_lanes(part[0]);
+    if (lane == 0) *sums = part[0];
+  }
+}
+
+// The first of n sums at which `before` + their running sum passes `target`, else the last that is above 0, else -1;
+// `before` takes the sums in front of it.  One warp.
+__device__ __forceinline__ int crossing(const Sum* sums, int n, const Sum& target, Sum& before) {
+  const int lane = threadIdx.x & 31;
+  Sum run = before;
+  int last = -1;
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const Sum x = i0 + lane < n ? sums[i0 + lane] : Sum{0.f, 0.f};
+    Sum end = upto_lane(x), front{__shfl_up_sync(kAll, end.hi, 1), __shfl_up_sync(kAll, end.lo, 1)};
+    if (lane == 0) front = {0.f, 0.f};
+    end.add(run);
+    front.add(run);
+    const uint32_t some = __ballot_sync(kAll, x.positive()), hit = some & __ballot_sync(kAll, end.above(target));
     const int who = hit ? __ffs(hit) - 1 : some ? 31 - __clz(some) : -1;
     if (who >= 0) {
       last = i0 + who;
-      at_last = run + __shfl_sync(kAll, end - x, who);
+      before = of_lane(front, who);
     }
     if (hit) break;
-    run += __shfl_sync(kAll, end, 31);
+    run = of_lane(end, 31);
   }
-  before = at_last;
   return last;
 }
 
-__global__ void __launch_bounds__(kVerifyThreads) verify_tree_kernel(const VerifyParams p) {
-  __shared__ VerifyShared s;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t b = blockIdx.x;
-  const NodeRange r = nodes_of(p.cu_seqlens_q, b, p.n_tok);
-  int32_t* keep = p.keep + b * p.max_keep;
-  int32_t* out = p.out_tokens + b * p.max_keep;
-  if (r.n == 0) {
-    for (int i = tid; i < p.max_keep; i += kVerifyThreads) keep[i] = out[i] = -1;
-    if (tid == 0) p.n_keep[b] = 0;
-    return;
-  }
-  const int n = static_cast<int>(min(r.n, static_cast<int64_t>(kMaxNodes)));
-  for (int i = tid; i < n; i += kVerifyThreads) {
-    const int64_t row = r.row0 + i;
-    const int32_t parent = i > 0 ? __ldg(p.parents + row) : -1, token = __ldg(p.tokens + row);
-    const bool tested = parent >= 0 && parent < i && token >= 0 && token < p.vocab;   // others are never tested
+enum { kWalkOn = 0, kSearch = 1, kLeave = 2 };
+
+struct VerifyShared {
+  int32_t parent[kWindow], token[kWindow], gone[kMaxNodes];
+  float u[kWindow], px[kWindow], qx[kWindow];
+  Sum sums[kMaxTiles];
+  Sum totals[2][kMaxCluster];     // of the cluster's CTAs; of two passes in turn
+  Sum target, before;
+  float c;
+  int cur, kept, n_gone, then, v0, v1, hit, last;
+};
+
+__device__ __forceinline__ void load_nodes(const VerifyParams& p, const NodeRange& r, int w0, int n, VerifyShared& s, int first, int step) {
+  for (int i = first; i < min(n - w0, kWindow); i += step) {
+    const int node = w0 + i;
+    const int64_t row = r.row0 + node;
+    const int32_t parent = node > 0 ? __ldg(p.parents + row) : -1, token = __ldg(p.tokens + row);
+    const bool tested = parent >= 0 && parent < node && token >= 0 && token < p.vocab;   // others are never tested
     s.parent[i] = tested ? parent : -1;
     s.token[i] = token;
     s.u[i] = __ldg(p.accept_u + row);
     s.px[i] = tested ? fmaxf(__ldg(p.target + (r.row0 + parent) * p.target_stride + token), 0.f) : 0.f;
     s.qx[i] = tested && p.draft ? __ldg(p.draft + (r.row0 + parent) * p.draft_stride + token) : 1.f;
   }
+}
+
+__global__ void __launch_bounds__(kVerifyThreads, 4) verify_tree_kernel(const VerifyParams p) {
+  __shared__ VerifyShared s;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = static_cast<int>(cluster_rank()), ranks = static_cast<int>(cluster_size());
+  const int64_t b = blockIdx.x / ranks;
+  const NodeRange r = nodes_of(p.cu_seqlens_q, b, p.n_tok);
+  int32_t* keep = p.keep + b * p.max_keep;
+  int32_t* out = p.out_tokens + b * p.max_keep;
+  if (r.n == 0) {
+    if (rank > 0) return;
+    for (int i = tid; i < p.max_keep; i += kVerifyThreads) keep[i] = out[i] = -1;
+    if (tid == 0) p.n_keep[b] = 0;
+    return;
+  }
+  cluster_arrive_relaxed();    // waited for before the first sum is sent: by then every CTA runs
+  const float sample_u = fmaxf(__ldg(p.sample_u + b), 0.f);
+  const int n = static_cast<int>(min(r.n, static_cast<int64_t>(kMaxNodes)));
+  load_nodes(p, r, 0, n, s, tid, kVerifyThreads);
   if (tid == 0) {
-    s.cur = 0;
-    s.kept = s.next = 1;
-    s.c = 0.f;
-    s.z = 1.0;
-    s.n_gone = 0;
+    s.hit = INT_MAX;
+    s.last = -1;
   }
   __syncthreads();
+  // the walk's state, in warp 0
+  int cur = 0, kept = 1, next = 1, w0 = 0, n_gone = 0;
+  float c = 0.f;
+  Sum z{1.f, 0.f};
+  bool summed = true;                   // Z is known
   Residual left;
-  for (;;) {
+  int first, behind;
+  for (int pass = 0;; ++pass) {
     // ---- the walk, to its end or to where Z has to be known
+    bool ask = false;
     if (warp == 0) {
-      int cur = s.cur, kept = s.kept, next = s.next, n_gone = s.n_gone;
-      float c = s.c;
-      double z = s.z;                   // below 0: not summed yet
-      bool ask = false;
       while (next < n && kept < p.max_keep) {
-        const int i = next + lane;
-        const uint32_t child = __ballot_sync(kAll, i < n && s.parent[i] == cur);
+        if (next >= w0 + kWindow) {
+          w0 += kWindow;
+          __syncwarp();
+          load_nodes(p, r, w0, n, s, lane, 32);
+          __syncwarp();
+        }
+        const int i = next - w0 + lane;
+        const uint32_t child = __ballot_sync(kAll, i < min(n - w0, kWindow) && s.parent[i] == cur);
         if (!child) {
-          next += 32;
+          next = min(next + 32, w0 + kWindow);
           continue;
         }
-        const int k = next + __ffs(child) - 1;
-        if (z < 0.0) {
-          next = k;
+        const int k = next - w0 + __ffs(child) - 1;
+        if (!summed) {
+          next = w0 + k;
           ask = true;
           break;
         }
@@ -261,121 +379,166 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_tree_kernel(const Verif
           for (int g = 0; g < n_gone; ++g)
             if (s.gone[g] == x) rx = 0.f;
         }
-        if (static_cast<double>(s.u[k]) * s.qx[k] * z < rx) {
-          if (lane == 0) {
-            keep[kept] = k;
+        // u q Z < r, the product in two floats
+        const float uq = s.u[k] * s.qx[k], low = fmaf(s.u[k], s.qx[k], -uq);
+        const float h = uq * z.hi, e = fmaf(uq, z.hi, -h) + fmaf(uq, z.lo, low * z.hi);
+        if ((rx - h) - e > 0.f) {
+          cur = w0 + k;
+          if (lane == 0 && rank == 0) {
+            keep[kept] = cur;
             out[kept - 1] = x;
           }
-          cur = k;
           ++kept;
           c = 0.f;
-          z = 1.0;
+          z = {1.f, 0.f};
           n_gone = 0;
         } else if (p.draft) {
-          c = static_cast<float>(c + z);
-          z = -1.0;
+          z.add(c);
+          c = z.hi + z.lo;
+          summed = false;
         } else {
           if (lane == 0) s.gone[n_gone] = x;
           ++n_gone;
-          z -= rx;
-          if (z < 0.0) z = 0.0;
+          z.add(-rx);
+          if (!z.positive()) z = {0.f, 0.f};
         }
-        next = k + 1;
+        next = w0 + k + 1;
         __syncwarp();
       }
-      __syncwarp();
       if (lane == 0) {
         s.cur = cur;
-        s.kept = kept;
-        s.next = next;
         s.n_gone = n_gone;
         s.c = c;
-        s.z = z;
-        s.ask = ask;
       }
     }
     __syncthreads();
     // ---- the sum of r
     left.p = p.target + (r.row0 + s.cur) * p.target_stride;
-    left.q = p.draft ? p.draft + (r.row0 + s.cur) * p.draft_stride : nullptr;
     left.c = s.c;
+    left.q = left.c > 0.f ? p.draft + (r.row0 + s.cur) * p.draft_stride : nullptr;
     left.gone = s.gone;
     left.n_gone = s.n_gone;
-    const int64_t each = (static_cast<int64_t>(p.vocab) + kVerifyWarps - 1) / kVerifyWarps;
-    const double mine = sum_of(left, min(warp * each, static_cast<int64_t>(p.vocab)), min((warp + 1) * each, static_cast<int64_t>(p.vocab)));
-    if (lane == 0) s.sums[warp] = mine;
-    __syncthreads();
-    double total = 0.0;
-    for (int w = 0; w < kVerifyWarps; ++w) total += s.sums[w];
-    if (s.ask) {
-      __syncthreads();
-      if (tid == 0) s.z = total;
-      __syncthreads();
-      continue;
+    // 16-byte loads, where p and q lie alike: counted from the first 16-byte boundary at or in front of the row
+    const bool wide = !left.q || ((reinterpret_cast<uintptr_t>(left.p) ^ reinterpret_cast<uintptr_t>(left.q)) & 15) == 0;
+    first = rank * p.each - static_cast<int>(reinterpret_cast<uintptr_t>(left.p) / 4 & 3);   // this CTA's part of the vocabulary
+    first = min(first, p.vocab);
+    behind = min(first + p.each, p.vocab);
+    const int tiles = (behind - first + p.tile - 1) / p.tile, mine = (tiles + kVerifyWarps - 1) / kVerifyWarps;
+    const int v0 = min(first + warp * mine * p.tile, behind), v1 = min(v0 + mine * p.tile, behind);
+    Sum* sums = s.sums + warp * mine;
+    if (wide) {
+      if (left.q) tile_sums<true, true>(left, v0, v1, p.tile, sums);
+      else tile_sums<false, true>(left, v0, v1, p.tile, sums);
+    } else {
+      if (left.q) tile_sums<true, false>(left, v0, v1, p.tile, sums);
+      else tile_sums<false, false>(left, v0, v1, p.tile, sums);
     }
-    if (total > 0.0 || (left.c == 0.f && left.n_gone == 0)) {
-      // ---- the last token: the range in which the running sum passes u * total, cut again until a warp searches it
-      const double target = static_cast<double>(fmaxf(__ldg(p.sample_u + b), 0.f)) * total;
-      int64_t v0 = 0, v1 = p.vocab, part = each;
-      double before = 0.0;
-      for (;;) {
-        if (warp == 0) {
-          const int at = crossing(s.sums, kVerifyWarps, target, before);
+    __syncthreads();
+    if (pass == 0) cluster_wait();
+    if (warp == 0) {
+      Sum sum{0.f, 0.f};
+      for (int i = lane; i < tiles; i += 32) sum.add(s.sums[i]);
+      add_lanes(sum);
+      if (lane < ranks) store_floats(map_to_rank(smem_u32(&s.totals[pass & 1][rank]), lane), sum.hi, sum.lo);
+      __syncwarp();
+    }
+    cluster_arrive();
+    cluster_wait();
+    if (warp == 0) {
+      const Sum* totals = s.totals[pass & 1];
+      Sum sum = lane < ranks ? totals[lane] : Sum{0.f, 0.f};
+      add_lanes(sum);
+      int then = kWalkOn;
+      if (ask) {
+        z = sum;
+        summed = true;
+      } else if (sum.positive() || (c == 0.f && n_gone == 0)) {
+        // the last token lies in the part of the CTA in which the running sum passes u * total
+        const float h = sample_u * sum.hi;
+        const Sum target{h, fmaf(sample_u, sum.hi, -h) + sample_u * sum.lo};
+        Sum before{0.f, 0.f};
+        const int owner = crossing(totals, ranks, target, before);
+        then = rank == max(owner, 0) ? kSearch : kLeave;
+        if (then == kSearch) {
+          const int at = owner < 0 ? -1 : crossing(s.sums, tiles, target, before);
           if (lane == 0) {
-            s.v0 = at < 0 ? -1 : v0 + at * part;
-            s.v1 = at < 0 ? -1 : min(v0 + (at + 1) * part, v1);
+            s.target = target;
             s.before = before;
+            s.kept = kept;
+            s.v0 = first + max(at, 0) * p.tile;
+            s.v1 = at < 0 ? s.v0 : min(s.v0 + p.tile, behind);
           }
         }
-        __syncthreads();
-        v0 = s.v0;
-        v1 = s.v1;
-        before = s.before;
-        if (v1 - v0 <= kScanLen) break;
-        part = (v1 - v0 + kVerifyWarps - 1) / kVerifyWarps;
-        const double sub = sum_of(left, min(v0 + warp * part, v1), min(v0 + (warp + 1) * part, v1));
-        __syncthreads();
-        if (lane == 0) s.sums[warp] = sub;
-        __syncthreads();
+      } else {   // nothing is left although p has not been used up (p <= C q everywhere): p itself
+        c = 0.f;
+        n_gone = 0;
+        next = n;
       }
-      if (warp == 0) {
-        int64_t token = -1;
-        for (int64_t a = v0; a >= 0 && a < v1; a += 32) {
-          const float x = a + lane < v1 ? left_of(left, a + lane) : 0.f;
-          double end = x;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const double u = __shfl_up_sync(kAll, end, o);
-            if (lane >= o) end += u;
-          }
-          const uint32_t hit = __ballot_sync(kAll, x > 0.f && before + end > target);
-          const uint32_t some = __ballot_sync(kAll, x > 0.f);
-          if (hit) {
-            token = a + __ffs(hit) - 1;
-            break;
-          }
-          if (some) token = a + 31 - __clz(some);
-          before += __shfl_sync(kAll, end, 31);
-        }
-        const int kept = s.kept;
-        if (lane == 0) {
-          keep[0] = 0;
-          out[kept - 1] = static_cast<int32_t>(token);
-          p.n_keep[b] = kept;
-        }
-        for (int i = kept + lane; i < p.max_keep; i += 32) keep[i] = out[i] = -1;
-      }
-      return;
-    }
-    // nothing is left although p has not been used up (p <= C q everywhere): p itself
-    __syncthreads();
-    if (tid == 0) {
-      s.c = 0.f;
-      s.n_gone = 0;
-      s.next = n;
+      if (lane == 0) s.then = then;
     }
     __syncthreads();
+    if (s.then == kLeave) return;
+    if (s.then == kSearch) break;
   }
+  // ---- a tile of more than kTile values is cut again; four values of the last one a thread
+  const Sum target = s.target;
+  Sum before = s.before;
+  int v0 = s.v0, v1 = s.v1;
+  while (v1 - v0 > kTile) {
+    const int part = (v1 - v0 + kVerifyWarps - 1) / kVerifyWarps, a = min(v0 + warp * part, v1), e = min(a + part, v1);
+    Sum sum{0.f, 0.f};
+    for (int v = max(a, 0) + lane; v < e; v += 32) sum.add(left_of(left, v));
+    add_lanes(sum);
+    __syncthreads();
+    if (lane == 0) s.sums[warp] = sum;
+    __syncthreads();
+    if (warp == 0) {
+      const int at = crossing(s.sums, kVerifyWarps, target, before);
+      if (lane == 0) {
+        s.before = before;
+        s.v0 = v0 + max(at, 0) * part;
+        s.v1 = at < 0 ? s.v0 : min(s.v0 + part, v1);
+      }
+    }
+    __syncthreads();
+    before = s.before;
+    v0 = s.v0;
+    v1 = s.v1;
+  }
+  float x[4];
+  Sum sum{0.f, 0.f};
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int v = v0 + 4 * tid + u;
+    x[u] = v >= 0 && v < v1 ? left_of(left, v) : 0.f;
+    sum.add(x[u]);
+  }
+  const Sum upto = upto_lane(sum);
+  __syncthreads();
+  if (lane == 31) s.sums[warp] = upto;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) before.add(s.sums[w]);
+  const Sum front{__shfl_up_sync(kAll, upto.hi, 1), __shfl_up_sync(kAll, upto.lo, 1)};
+  if (lane > 0) before.add(front);
+  int hit = INT_MAX, last = -1;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    before.add(x[u]);
+    if (x[u] > 0.f) {
+      last = v0 + 4 * tid + u;
+      if (hit == INT_MAX && before.above(target)) hit = last;
+    }
+  }
+  if (hit < INT_MAX) atomicMin(&s.hit, hit);
+  if (last >= 0) atomicMax(&s.last, last);
+  __syncthreads();
+  const int end = s.kept;
+  if (tid == 0) {
+    keep[0] = 0;
+    out[end - 1] = s.hit < INT_MAX ? s.hit : s.last;
+    p.n_keep[b] = end;
+  }
+  for (int i = end + tid; i < p.max_keep; i += kVerifyThreads) keep[i] = out[i] = -1;
 }
 
 // ------------------------------------------------------------------------ commit
@@ -559,8 +722,8 @@ smla_status sparse_mla_verify_tree(const float* target_probs, int64_t target_str
                                    const int32_t* cu_seqlens_q, const float* accept_u, const float* sample_u,
                                    int32_t* keep, int32_t* out_tokens, int32_t* n_keep, int64_t n_req, int64_t n_tok,
                                    int vocab, int max_keep, smla_stream_t stream) {
-  if (n_req < 0 || n_req > INT32_MAX || n_tok < 0 || n_tok > INT32_MAX || vocab < 1 || max_keep < 1 ||
-      n_req > INT32_MAX / max_keep)
+  if (n_req < 0 || n_req > INT32_MAX || n_tok < 0 || n_tok > INT32_MAX || vocab < 1 || vocab > kMaxVocab ||
+      max_keep < 1 || n_req > INT32_MAX / max_keep)
     return SMLA_ERR_BAD_SHAPE;
   if (n_req == 0) return SMLA_OK;
   if (!cu_seqlens_q || !sample_u || !keep || !out_tokens || !n_keep ||
@@ -580,10 +743,28 @@ smla_status sparse_mla_verify_tree(const float* target_probs, int64_t target_str
                      {cu_seqlens_q, reqs + 4}, {accept_u, toks}, {sample_u, reqs}};
   const Span written[] = {{keep, reqs * max_keep}, {out_tokens, reqs * max_keep}, {n_keep, reqs}};
   if (any_overlap(in, written)) return SMLA_ERR_BAD_SHAPE;
-  const VerifyParams p{target_probs, draft_probs, tokens, parents, cu_seqlens_q, accept_u, sample_u, keep, out_tokens,
-                       n_keep, target_stride, draft_stride, n_req, n_tok, vocab, max_keep};
-  verify_tree_kernel<<<static_cast<unsigned>(n_req), kVerifyThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
-  return cudaGetLastError() == cudaSuccess ? SMLA_OK : SMLA_ERR_LAUNCH;
+  VerifyParams p{target_probs, draft_probs, tokens, parents, cu_seqlens_q, accept_u, sample_u, keep, out_tokens,
+                       n_keep, target_stride, draft_stride, n_req, n_tok, vocab, max_keep, 0, 0};
+  // A cluster of up to eight CTAs, while there is work for each and all clusters run at once (four CTAs an SM)
+  int ranks = 1;
+  while (ranks < kMaxCluster && vocab > ranks * kTile && n_req * ranks * 2 <= 4 * 152) ranks *= 2;
+  p.each = ((vocab + 3 + ranks - 1) / ranks + 3) / 4 * 4;
+  p.tile = (p.each + kVerifyWarps - 1) / kVerifyWarps;
+  p.tile = p.tile > kTile ? kTile : p.tile;
+  if (p.each > p.tile * kMaxTiles) p.tile = (p.each + kMaxTiles - 1) / kMaxTiles;
+  p.tile = (p.tile + 255) / 256 * 256;
+  cudaLaunchAttribute cluster{};
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim.x = ranks;
+  cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  if (n_req > INT32_MAX / ranks) return SMLA_ERR_BAD_SHAPE;
+  cfg.gridDim = dim3(static_cast<unsigned>(n_req * ranks));
+  cfg.blockDim = dim3(kVerifyThreads);
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cfg.attrs = &cluster;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, verify_tree_kernel, p) == cudaSuccess ? SMLA_OK : SMLA_ERR_LAUNCH;
 }
 
 smla_status sparse_mla_commit_tree(const int32_t* keep, const int32_t* n_keep, int max_keep, const int32_t* cu_seqlens_q,

@@ -106,7 +106,7 @@ def verify(lib, **kw):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(n_req=-1), SHAPE), (dict(n_tok=-1), SHAPE), (dict(n_req=1 << 31), SHAPE), (dict(n_tok=1 << 31), SHAPE),
-    (dict(vocab=0), SHAPE), (dict(max_keep=0), SHAPE), (dict(n_req=1 << 20, max_keep=1 << 11), SHAPE),
+    (dict(vocab=0), SHAPE), (dict(vocab=(1 << 30) + 1, ts=1 << 31, ds=1 << 31), SHAPE), (dict(max_keep=0), SHAPE), (dict(n_req=1 << 20, max_keep=1 << 11), SHAPE),
     (dict(ts=1000), SHAPE), (dict(ds=1000), SHAPE), (dict(ts=-1040), SHAPE), (dict(ts=1 << 61), SHAPE), (dict(ds=1 << 61), SHAPE),
     *[({n: None}, NULL) for n in VERIFY if n != "draft"], *[({n: VERIFY[n] + 2}, MISALIGNED) for n in VERIFY],
 ])

@@ -456,6 +456,8 @@ def test_verify_many_requests(draft, kind):
 def test_verify_large_vocabulary():
     verify_check(verify_case(5, [4, 3, 7], 151_643, kind="star", apart=2.0))
     verify_check(verify_case(6, [4, 3, 7], 128_000, False, "star"))
+    for vocab in (5_000_003, 3_000_000):
+        verify_check(verify_case(7, [3, 2], vocab, vocab % 2 == 1, "star", scale=0.5))
 
 
 def test_verify_rows_far_apart():
