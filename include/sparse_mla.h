@@ -466,13 +466,13 @@ smla_status sparse_mla_verify_tree(const float* target_probs, int64_t target_str
  *   kv_pool      [n_layers, pool_rows, d_qk] bf16, layers layer_stride elements apart (a multiple of 8, at least
  *                pool_rows * d_qk), 16-byte aligned; n_layers 0: no rows are moved.  Rows from before on lie in pages of
  *                the request's own.
- *   free_pages   [n_free] int32 (written below free_start), or NULL: no page goes back.  sparse_mla_plan_pages hands out
+ *   free_pages   [n_free] int32 (written below free_start); NULL or empty: no page goes back.  sparse_mla_plan_pages hands out
  *                from index free_start on; pages come back in front of it, request by request and column by
  *                column, each to the index below the last.
  *   free_start   [1] int32 or NULL for n_free (clamped to [0, n_free])
  *   seqlens      [n_req] int32 (written)
- *   counts       [3] int32 (written): tokens kept, the next free_start (0 without free_pages), pages for which there
- *                was no room in front of free_start (they stay in the table only)
+ *   counts       [3] int32 (written): tokens kept, the next free_start, pages for which there was no room in front of
+ *                free_start (they stay in the table only); the latter two 0 without free_pages
  * counts + 1 is the next sparse_mla_plan_pages' free_start, seqlens its seqlens.  All other pointers 4-byte aligned; those
  * of empty arrays may be NULL.  The stride of a single layer is not looked at.  SMLA_ERR_BAD_SHAPE when an output
  * overlaps an input or another output.

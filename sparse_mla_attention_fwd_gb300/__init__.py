@@ -66,6 +66,7 @@ def _stream_handle(stream, device):
 # the current stream's handle on a device; a stream object in between costs two microseconds
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 # torch.empty on the current device without its argument parsing, which is nearly half of its 1.5 microseconds
 try:
     from torch._C._dynamo.guards import _empty_strided_cuda as _empty_strided
@@ -408,6 +409,24 @@ def _dense(t, name, dtype, dev=None):
     raise TypeError(f"{name} must be a torch.Tensor")
 
 
+def _ready(index, dtype, *tensors):
+    """Whether these are dense tensors of this type on this device: the usual case, in one test for all."""
+    for t in tensors:
+        if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+            return False
+    return True
+
+
+def _here(t, stream):
+    """The device index of a call's first tensor when the call can go on as it is; else -1: it is no GPU tensor, or the call has
+    to go through _on_device."""
+    if stream is None and isinstance(t, torch.Tensor):
+        index = t.get_device()
+        if index >= 0 and _current_device() == index:
+            return index
+    return -1
+
+
 def _int_output(t, name, n, dev):
     """An int32 output [n]: the caller's, or a new one on the current device."""
     if t is None:
@@ -560,15 +579,17 @@ def sparse_mla_append_kv(c_kv, k_pe, slots, kv_pool, norm_weight=None, eps=1e-6,
     return kv_pool
 
 
-def _dense_attention_args(q, kv_pool, block_table, cu_seqlens_q, seqlens_k, attn_sink, sm_scale, d_v, out, lse, max_logits,
-                          workspace, lib, dev):
+def _dense_attention_args(index, q, kv_pool, block_table, cu_seqlens_q, seqlens_k, attn_sink, sm_scale, d_v, out, lse,
+                          max_logits, workspace, lib):
     """Checks of the dense attentions' tensors; returns the sizes, the outputs (allocated when not given), the scale and
     the workspace."""
     bf16, i32, f32 = torch.bfloat16, torch.int32, torch.float32
-    _dense(kv_pool, "kv_pool", bf16, dev)
-    _dense(block_table, "block_table", i32, dev)
-    _dense(cu_seqlens_q, "cu_seqlens_q", i32, dev)
-    _dense(seqlens_k, "seqlens_k", i32, dev)
+    if not _ready(index, bf16, q, kv_pool) or not _ready(index, i32, block_table, cu_seqlens_q, seqlens_k):
+        dev = _dense(q, "q", bf16)
+        _dense(kv_pool, "kv_pool", bf16, dev)
+        _dense(block_table, "block_table", i32, dev)
+        _dense(cu_seqlens_q, "cu_seqlens_q", i32, dev)
+        _dense(seqlens_k, "seqlens_k", i32, dev)
     q_shape, pool_shape, table_shape = q.shape, kv_pool.shape, block_table.shape
     if len(q_shape) != 3:
         raise ValueError("q must be [n_tok, h, d_qk]")
@@ -582,7 +603,7 @@ def _dense_attention_args(q, kv_pool, block_table, cu_seqlens_q, seqlens_k, attn
     if seqlens_k.numel() != n_req or cu_seqlens_q.numel() != n_req + 1:
         raise ValueError("seqlens_k must have n_req entries and cu_seqlens_q n_req + 1")
     if attn_sink is not None:
-        _dense(attn_sink, "attn_sink", f32, dev)
+        _dense(attn_sink, "attn_sink", f32, q.device)
         if attn_sink.numel() != h_q:
             raise ValueError("attn_sink must have h entries")
     if sm_scale is None:
@@ -597,7 +618,7 @@ def _dense_attention_args(q, kv_pool, block_table, cu_seqlens_q, seqlens_k, attn
         ws_bytes = lib.sparse_mla_chunk_workspace_size(n_tok, h_q)
         workspace = _empty_strided((ws_bytes,), (1,), torch.uint8)
     else:
-        _dense(workspace, "workspace", torch.uint8, dev)
+        _dense(workspace, "workspace", torch.uint8, q.device)
         ws_bytes = workspace.numel()
     return n_tok, h_q, d_qk, pool_rows, n_req, max_blocks, out, lse, max_logits, sm_scale, workspace, ws_bytes
 
@@ -614,17 +635,18 @@ def sparse_mla_chunk_fwd_paged(q, kv_pool, block_table, cu_seqlens_q, seqlens_k,
     sparse_mla_chunk_workspace_size bytes, 256-byte aligned) is allocated here when not given; calls
     that may overlap must not share one."""
     lib = load_library()
-    dev = _dense(q, "q", torch.bfloat16)
-    if stream is not None or torch.cuda.current_device() != dev.index:
+    index = _here(q, stream)
+    if index < 0:
+        dev = _dense(q, "q", torch.bfloat16)
         return _on_device(sparse_mla_chunk_fwd_paged, dev, stream, q, kv_pool, block_table, cu_seqlens_q, seqlens_k, page_block,
                           causal, attn_sink, sm_scale, d_v, out, lse, max_logits, workspace)
     n_tok, h_q, d_qk, pool_rows, n_req, max_blocks, out, lse, max_logits, sm_scale, workspace, ws_bytes = _dense_attention_args(
-        q, kv_pool, block_table, cu_seqlens_q, seqlens_k, attn_sink, sm_scale, d_v, out, lse, max_logits, workspace, lib, dev)
+        index, q, kv_pool, block_table, cu_seqlens_q, seqlens_k, attn_sink, sm_scale, d_v, out, lse, max_logits, workspace, lib)
     rc = lib.sparse_mla_chunk_fwd_paged(
         q.data_ptr(), kv_pool.data_ptr(), pool_rows, block_table.data_ptr(), max_blocks, int(page_block),
         cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), n_req, 1 if causal else 0, _ptr(attn_sink), float(sm_scale), int(d_v),
         out.data_ptr(), lse.data_ptr(), max_logits.data_ptr(), n_tok, h_q, d_qk, workspace.data_ptr(), ws_bytes,
-        _raw_stream(dev.index))
+        _raw_stream(index))
     if rc != 0:
         raise SmlaError(rc, "sparse_mla_chunk_fwd_paged")
     return out, lse, max_logits
@@ -638,11 +660,14 @@ def sparse_mla_plan_tree(parents, cu_seqlens_q, seqlens_k, mask_words, tree_mask
     :func:`sparse_mla_append_kv`), allocated here when not given.  Rows of no request get 0 and -1."""
     lib = load_library()
     i32 = torch.int32
-    dev = _dense(parents, "parents", i32)
-    if stream is not None or torch.cuda.current_device() != dev.index:
+    index = _here(parents, stream)
+    if index < 0:
+        dev = _dense(parents, "parents", i32)
         return _on_device(sparse_mla_plan_tree, dev, stream, parents, cu_seqlens_q, seqlens_k, mask_words, tree_mask, positions)
-    _dense(cu_seqlens_q, "cu_seqlens_q", i32, dev)
-    _dense(seqlens_k, "seqlens_k", i32, dev)
+    if not _ready(index, i32, parents, cu_seqlens_q, seqlens_k):
+        dev = _dense(parents, "parents", i32)
+        _dense(cu_seqlens_q, "cu_seqlens_q", i32, dev)
+        _dense(seqlens_k, "seqlens_k", i32, dev)
     n_tok, n_req, mask_words = parents.numel(), seqlens_k.numel(), int(mask_words)
     if cu_seqlens_q.numel() != n_req + 1:
         raise ValueError("cu_seqlens_q must have n_req + 1 entries")
@@ -651,12 +676,13 @@ def sparse_mla_plan_tree(parents, cu_seqlens_q, seqlens_k, mask_words, tree_mask
     if tree_mask is None:
         tree_mask = _empty_strided((n_tok, mask_words), (mask_words, 1), i32)
     else:
-        _dense(tree_mask, "tree_mask", i32, dev)
+        _dense(tree_mask, "tree_mask", i32, parents.device)
         if tree_mask.shape != (n_tok, mask_words):
             raise ValueError(f"tree_mask must be [{n_tok}, {mask_words}], got {list(tree_mask.shape)}")
-    positions = _int_output(positions, "positions", n_tok, dev)
+    positions = _empty_strided((n_tok,), (1,), i32) if positions is None else \
+        _int_output(positions, "positions", n_tok, parents.device)
     rc = lib.sparse_mla_plan_tree(parents.data_ptr(), cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), tree_mask.data_ptr(),
-                                  positions.data_ptr(), n_req, n_tok, mask_words, _raw_stream(dev.index))
+                                  positions.data_ptr(), n_req, n_tok, mask_words, _raw_stream(index))
     if rc != 0:
         raise SmlaError(rc, "sparse_mla_plan_tree")
     return tree_mask, positions
@@ -669,13 +695,15 @@ def sparse_mla_tree_fwd_paged(q, kv_pool, block_table, cu_seqlens_q, seqlens_k, 
     :func:`sparse_mla_plan_tree`; any mask will do).  Everything else, workspace and returned values among it, is as
     there."""
     lib = load_library()
-    dev = _dense(q, "q", torch.bfloat16)
-    if stream is not None or torch.cuda.current_device() != dev.index:
+    index = _here(q, stream)
+    if index < 0:
+        dev = _dense(q, "q", torch.bfloat16)
         return _on_device(sparse_mla_tree_fwd_paged, dev, stream, q, kv_pool, block_table, cu_seqlens_q, seqlens_k, tree_mask,
                           page_block, attn_sink, sm_scale, d_v, out, lse, max_logits, workspace)
     n_tok, h_q, d_qk, pool_rows, n_req, max_blocks, out, lse, max_logits, sm_scale, workspace, ws_bytes = _dense_attention_args(
-        q, kv_pool, block_table, cu_seqlens_q, seqlens_k, attn_sink, sm_scale, d_v, out, lse, max_logits, workspace, lib, dev)
-    _dense(tree_mask, "tree_mask", torch.int32, dev)
+        index, q, kv_pool, block_table, cu_seqlens_q, seqlens_k, attn_sink, sm_scale, d_v, out, lse, max_logits, workspace, lib)
+    if not _ready(index, torch.int32, tree_mask):
+        _dense(tree_mask, "tree_mask", torch.int32, q.device)
     mask_shape = tree_mask.shape
     if len(mask_shape) != 2 or mask_shape[0] != n_tok:
         raise ValueError("tree_mask must be [n_tok, words]")
@@ -683,23 +711,25 @@ def sparse_mla_tree_fwd_paged(q, kv_pool, block_table, cu_seqlens_q, seqlens_k, 
         q.data_ptr(), kv_pool.data_ptr(), pool_rows, block_table.data_ptr(), max_blocks, int(page_block),
         cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), n_req, tree_mask.data_ptr(), mask_shape[1], _ptr(attn_sink),
         float(sm_scale), int(d_v), out.data_ptr(), lse.data_ptr(), max_logits.data_ptr(), n_tok, h_q, d_qk,
-        workspace.data_ptr(), ws_bytes, _raw_stream(dev.index))
+        workspace.data_ptr(), ws_bytes, _raw_stream(index))
     if rc != 0:
         raise SmlaError(rc, "sparse_mla_tree_fwd_paged")
     return out, lse, max_logits
 
 
-def _probs(t, name, n_tok, vocab, dev):
-    """The row stride of an fp32 tensor [n_tok, vocab] whose last dimension is contiguous."""
+def _probs(t, name, n_tok, vocab, index):
+    """The row stride of an fp32 tensor [n_tok, vocab] whose last dimension is contiguous, and its vocab (any, if given as 0)."""
+    if isinstance(t, torch.Tensor) and t.dtype is torch.float32 and t.get_device() == index:
+        shape = t.shape
+        if len(shape) == 2 and shape[0] == n_tok and shape[1] > 0 and (shape[1] == vocab or not vocab):
+            strides = t.stride()
+            if strides[1] == 1 or shape[1] == 1 or n_tok == 0:
+                return strides[0], shape[1]
+            raise ValueError(f"{name} must be contiguous in its last dimension")
+        raise ValueError(f"{name} must be [{n_tok}, {vocab or 'vocab'}], got {list(shape)}")
     if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32:
         raise TypeError(f"{name} must be a torch.float32 tensor")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if t.dim() != 2 or t.shape[0] != n_tok or (vocab is not None and t.shape[1] != vocab) or t.shape[1] < 1:
-        raise ValueError(f"{name} must be [{n_tok}, {'vocab' if vocab is None else vocab}], got {list(t.shape)}")
-    if t.stride(1) != 1 and t.numel() > 0 and t.shape[1] > 1:
-        raise ValueError(f"{name} must be contiguous in its last dimension")
-    return t.stride(0)
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
 
 
 def sparse_mla_verify_tree(target_probs, tokens, parents, cu_seqlens_q, accept_u, sample_u, max_keep, draft_probs=None,
@@ -714,14 +744,17 @@ def sparse_mla_verify_tree(target_probs, tokens, parents, cu_seqlens_q, accept_u
     follow the target's distribution.  See the C header for the exact rules."""
     lib = load_library()
     i32, f32 = torch.int32, torch.float32
-    dev = _dense(tokens, "tokens", i32)
-    if stream is not None or torch.cuda.current_device() != dev.index:
+    index = _here(tokens, stream)
+    if index < 0:
+        dev = _dense(tokens, "tokens", i32)
         return _on_device(sparse_mla_verify_tree, dev, stream, target_probs, tokens, parents, cu_seqlens_q, accept_u, sample_u,
                           max_keep, draft_probs, keep, out_tokens, n_keep)
-    _dense(parents, "parents", i32, dev)
-    _dense(cu_seqlens_q, "cu_seqlens_q", i32, dev)
-    _dense(accept_u, "accept_u", f32, dev)
-    _dense(sample_u, "sample_u", f32, dev)
+    if not _ready(index, i32, tokens, parents, cu_seqlens_q) or not _ready(index, f32, accept_u, sample_u):
+        dev = _dense(tokens, "tokens", i32)
+        _dense(parents, "parents", i32, dev)
+        _dense(cu_seqlens_q, "cu_seqlens_q", i32, dev)
+        _dense(accept_u, "accept_u", f32, dev)
+        _dense(sample_u, "sample_u", f32, dev)
     n_tok, n_req, max_keep = tokens.numel(), sample_u.numel(), int(max_keep)
     if parents.numel() != n_tok or accept_u.numel() != n_tok:
         raise ValueError("parents and accept_u must have one entry per token")
@@ -729,25 +762,46 @@ def sparse_mla_verify_tree(target_probs, tokens, parents, cu_seqlens_q, accept_u
         raise ValueError("cu_seqlens_q must have one entry more than sample_u")
     if max_keep < 1:
         raise ValueError("max_keep must be at least 1")
-    t_stride = _probs(target_probs, "target_probs", n_tok, None, dev)
-    vocab = target_probs.shape[1]
-    d_stride = 0 if draft_probs is None else _probs(draft_probs, "draft_probs", n_tok, vocab, dev)
-    if keep is None:
-        keep = _empty_strided((n_req, max_keep), (max_keep, 1), i32)
-    if out_tokens is None:
-        out_tokens = _empty_strided((n_req, max_keep), (max_keep, 1), i32)
-    for t, name in ((keep, "keep"), (out_tokens, "out_tokens")):
-        _dense(t, name, i32, dev)
-        if t.shape != (n_req, max_keep):
-            raise ValueError(f"{name} must be [{n_req}, {max_keep}], got {list(t.shape)}")
-    n_keep = _int_output(n_keep, "n_keep", n_req, dev)
+    t_stride, vocab = _probs(target_probs, "target_probs", n_tok, 0, index)
+    d_stride, draft = 0, None
+    if draft_probs is not None:
+        d_stride, draft = _probs(draft_probs, "draft_probs", n_tok, vocab, index)[0], draft_probs.data_ptr()
+    if keep is None and out_tokens is None and n_keep is None:
+        size, strides = (n_req, max_keep), (max_keep, 1)
+        keep, out_tokens = _empty_strided(size, strides, i32), _empty_strided(size, strides, i32)
+        n_keep = _empty_strided((n_req,), (1,), i32)
+    else:
+        dev = tokens.device
+        keep, out_tokens = (torch.empty((n_req, max_keep), dtype=i32, device=dev) if t is None else t for t in (keep, out_tokens))
+        for t, name in ((keep, "keep"), (out_tokens, "out_tokens")):
+            _dense(t, name, i32, dev)
+            if t.shape != (n_req, max_keep):
+                raise ValueError(f"{name} must be [{n_req}, {max_keep}], got {list(t.shape)}")
+        n_keep = _int_output(n_keep, "n_keep", n_req, dev)
     rc = lib.sparse_mla_verify_tree(
-        target_probs.data_ptr(), t_stride, _ptr(draft_probs), d_stride, tokens.data_ptr(), parents.data_ptr(),
-        cu_seqlens_q.data_ptr(), accept_u.data_ptr(), sample_u.data_ptr(), keep.data_ptr(), out_tokens.data_ptr(),
-        n_keep.data_ptr(), n_req, n_tok, vocab, max_keep, _raw_stream(dev.index))
+        target_probs.data_ptr(), t_stride, draft, d_stride, tokens.data_ptr(), parents.data_ptr(), cu_seqlens_q.data_ptr(),
+        accept_u.data_ptr(), sample_u.data_ptr(), keep.data_ptr(), out_tokens.data_ptr(), n_keep.data_ptr(), n_req, n_tok, vocab,
+        max_keep, _raw_stream(index))
     if rc != 0:
         raise SmlaError(rc, "sparse_mla_verify_tree")
     return keep, out_tokens, n_keep
+
+
+def _layers(kv_pool, index):
+    """Address, layers, layer stride, rows of a layer and d_qk of a cache [rows, 1, d_qk] or [layers, rows, 1, d_qk] that is
+    contiguous within a layer."""
+    if isinstance(kv_pool, torch.Tensor) and kv_pool.dtype is torch.bfloat16 and kv_pool.get_device() == index:
+        shape, strides = kv_pool.shape, kv_pool.stride()
+        if len(shape) in (3, 4) and shape[-2] == 1 and shape[-1] in (512, 576):
+            rows, d_qk = shape[-3], shape[-1]
+            if strides[-1] != 1 or (rows > 1 and strides[-3] != d_qk):
+                raise ValueError("kv_pool must be contiguous within a layer")
+            layers, layer_stride = (shape[0], strides[0]) if len(shape) == 4 else (1, 0)
+            return kv_pool.data_ptr(), layers, layer_stride, rows, d_qk
+        raise ValueError("kv_pool must be [rows, 1, d_qk] or [layers, rows, 1, d_qk] with d_qk 512 or 576")
+    if not isinstance(kv_pool, torch.Tensor) or kv_pool.dtype is not torch.bfloat16:
+        raise TypeError("kv_pool must be a torch.bfloat16 tensor")
+    raise ValueError(f"kv_pool is on {kv_pool.device}, expected cuda:{index}")
 
 
 def sparse_mla_commit_tree(keep, n_keep, cu_seqlens_q, seqlens_k, block_table, kv_pool, page_block=64, free_pages=None,
@@ -762,14 +816,17 @@ def sparse_mla_commit_tree(keep, n_keep, cu_seqlens_q, seqlens_k, block_table, k
     per layer and give free_pages in one of the calls."""
     lib = load_library()
     i32 = torch.int32
-    dev = _dense(keep, "keep", i32)
-    if stream is not None or torch.cuda.current_device() != dev.index:
+    index = _here(keep, stream)
+    if index < 0:
+        dev = _dense(keep, "keep", i32)
         return _on_device(sparse_mla_commit_tree, dev, stream, keep, n_keep, cu_seqlens_q, seqlens_k, block_table, kv_pool,
                           page_block, free_pages, free_start, seqlens, counts)
-    _dense(n_keep, "n_keep", i32, dev)
-    _dense(cu_seqlens_q, "cu_seqlens_q", i32, dev)
-    _dense(seqlens_k, "seqlens_k", i32, dev)
-    _dense(block_table, "block_table", i32, dev)
+    if not _ready(index, i32, keep, n_keep, cu_seqlens_q, seqlens_k, block_table):
+        dev = _dense(keep, "keep", i32)
+        _dense(n_keep, "n_keep", i32, dev)
+        _dense(cu_seqlens_q, "cu_seqlens_q", i32, dev)
+        _dense(seqlens_k, "seqlens_k", i32, dev)
+        _dense(block_table, "block_table", i32, dev)
     n_req, keep_shape, table_shape = seqlens_k.numel(), keep.shape, block_table.shape
     if len(keep_shape) != 2 or keep_shape[0] != n_req or keep_shape[1] < 1 or n_keep.numel() != n_req:
         raise ValueError("keep must be [n_req, max_keep] and n_keep have n_req entries")
@@ -777,33 +834,23 @@ def sparse_mla_commit_tree(keep, n_keep, cu_seqlens_q, seqlens_k, block_table, k
         raise ValueError("cu_seqlens_q must have n_req + 1 entries")
     if len(table_shape) != 2 or table_shape[0] != n_req:
         raise ValueError("block_table must be [n_req, max_blocks]")
-    layers = layer_stride = pool_rows = d_qk = 0
-    if kv_pool is not None:
-        if not isinstance(kv_pool, torch.Tensor) or kv_pool.dtype is not torch.bfloat16:
-            raise TypeError("kv_pool must be a torch.bfloat16 tensor")
-        if kv_pool.device != dev:
-            raise ValueError(f"kv_pool is on {kv_pool.device}, expected {dev}")
-        shape = kv_pool.shape
-        if len(shape) not in (3, 4) or shape[-2] != 1 or shape[-1] not in (512, 576):
-            raise ValueError("kv_pool must be [rows, 1, d_qk] or [layers, rows, 1, d_qk] with d_qk 512 or 576")
-        layers, pool_rows, d_qk = shape[0] if len(shape) == 4 else 1, shape[-3], shape[-1]
-        layer_stride = kv_pool.stride(0) if len(shape) == 4 else 0
-        strides = kv_pool.stride()
-        if kv_pool.numel() > 0 and (strides[-1] != 1 or (pool_rows > 1 and strides[-3] != d_qk)):
-            raise ValueError("kv_pool must be contiguous within a layer")
-    n_free = 0
+    pool, layers, layer_stride, pool_rows, d_qk = (None, 0, 0, 0, 0) if kv_pool is None else _layers(kv_pool, index)
+    free, n_free = None, 0
     if free_pages is not None:
-        _dense(free_pages, "free_pages", i32, dev)
-        n_free = free_pages.numel()
+        if not _ready(index, i32, free_pages):
+            _dense(free_pages, "free_pages", i32, keep.device)
+        free, n_free = free_pages.data_ptr(), free_pages.numel()
     if free_start is not None:
-        _dense(free_start, "free_start", i32, dev)
+        if not _ready(index, i32, free_start):
+            _dense(free_start, "free_start", i32, keep.device)
         if free_start.numel() != 1:
             raise ValueError("free_start must have one entry")
-    seqlens, counts = _int_output(seqlens, "seqlens", n_req, dev), _int_output(counts, "counts", 3, dev)
+    seqlens = _empty_strided((n_req,), (1,), i32) if seqlens is None else _int_output(seqlens, "seqlens", n_req, keep.device)
+    counts = _empty_strided((3,), (1,), i32) if counts is None else _int_output(counts, "counts", 3, keep.device)
     rc = lib.sparse_mla_commit_tree(
         keep.data_ptr(), n_keep.data_ptr(), keep_shape[1], cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), block_table.data_ptr(),
-        table_shape[1], int(page_block), n_req, _ptr(kv_pool), layers, layer_stride, pool_rows, d_qk, _ptr(free_pages), n_free,
-        _ptr(free_start), seqlens.data_ptr(), counts.data_ptr(), _raw_stream(dev.index))
+        table_shape[1], int(page_block), n_req, pool, layers, layer_stride, pool_rows, d_qk, free, n_free, _ptr(free_start),
+        seqlens.data_ptr(), counts.data_ptr(), _raw_stream(index))
     if rc != 0:
         raise SmlaError(rc, "sparse_mla_commit_tree")
     return seqlens, counts

@@ -549,6 +549,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_tree_kernel(const Ve
 // CTA 0 does the bookkeeping instead: lengths, and the pages behind them back in front of the free list's start.
 constexpr int kCommitThreads = 256;
 constexpr int kRowsInFlight = 4;
+constexpr int kFewColumns = 4;        // of a request's table, that a thread gives back by itself
 
 struct CommitParams {
   const int32_t* keep;
@@ -557,7 +558,7 @@ struct CommitParams {
   const int32_t* seqlens_k;
   const int32_t* block_table;
   __nv_bfloat16* pool;
-  int32_t* free_pages;          // or null: no page is given back
+  int32_t* free_pages;          // null: no page is given back
   const int32_t* free_start;    // or null: n_free
   int32_t* seqlens;
   int32_t* counts;
@@ -591,23 +592,52 @@ __device__ __forceinline__ int64_t columns_of(int64_t len, const CommitParams& p
   return min((len + p.page_block - 1) / p.page_block, static_cast<int64_t>(p.max_blocks));
 }
 
+// Calls put(page, k) for the pages of a request's table columns [first, last), in order, k counting the mapped ones; returns how
+// many there are.  A thread does its own request's few columns by itself; those with more (requests that are done) are done by
+// the warp, one request after the other.
+template <typename Put>
+__device__ __forceinline__ int64_t for_pages(const CommitParams& p, int64_t b, int64_t first, int64_t last, Put put) {
+  const int lane = threadIdx.x & 31;
+  int64_t count = 0;
+  const bool few = last - first <= kFewColumns;
+  if (few)
+    for (int64_t col = first; col < last; ++col) {
+      const int32_t page = __ldg(p.block_table + b * p.max_blocks + col);
+      if (page >= 0) put(page, count++, lane);
+    }
+  for (uint32_t many = __ballot_sync(kAll, !few); many; many &= many - 1) {
+    const int of = __ffs(many) - 1;
+    const int64_t bo = __shfl_sync(kAll, b, of), c1 = __shfl_sync(kAll, last, of);
+    int64_t found = 0;
+    for (int64_t c0 = __shfl_sync(kAll, first, of); c0 < c1; c0 += 32) {
+      const int32_t page = c0 + lane < c1 ? __ldg(p.block_table + bo * p.max_blocks + c0 + lane) : -1;
+      const uint32_t mapped = __ballot_sync(kAll, page >= 0);
+      if (page >= 0) put(page, found + __popc(mapped & ((1u << lane) - 1u)), of);
+      found += __popc(mapped);
+    }
+    if (lane == of) count = found;
+  }
+  return count;
+}
+
 __device__ void commit_lengths(const CommitParams& p) {
   __shared__ int64_t warp_sum[2][kCommitThreads / 32];
+  __shared__ int64_t place[kCommitThreads];     // of a request's first page, counted down from the list's start
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t start = p.free_pages ? min(max(p.free_start ? static_cast<int64_t>(__ldg(p.free_start)) : p.n_free, int64_t{0}), p.n_free) : 0;
   int64_t pages = 0, tokens = 0;
   for (int64_t b0 = 0; b0 < p.n_req; b0 += kCommitThreads) {
     const int64_t b = b0 + tid;
     Kept k{0, 0, 0};
-    int64_t first = 0, last = 0, back = 0;
+    int64_t first = 0, last = 0;
     if (b < p.n_req) {
       k = kept_of(p, b);
       const int64_t len = k.n < 0 ? 0 : max(k.before + k.n, int64_t{0});
       p.seqlens[b] = static_cast<int32_t>(len);
       first = columns_of(len, p);
       last = p.free_pages ? columns_of(k.n_k, p) : first;
-      for (int64_t col = first; col < last; ++col) back += __ldg(p.block_table + b * p.max_blocks + col) >= 0;
     }
+    const int64_t back = for_pages(p, b, first, last, [](int32_t, int64_t, int) {});
     int64_t end = back, kept = max(k.n, int64_t{0});
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -628,12 +658,12 @@ __device__ void commit_lengths(const CommitParams& p) {
       pages += warp_sum[0][w];
       tokens += warp_sum[1][w];
     }
-    for (int64_t col = first; col < last; ++col) {
-      const int32_t page = __ldg(p.block_table + b * p.max_blocks + col);
-      if (page < 0) continue;
-      if (at < start) p.free_pages[start - 1 - at] = page;
-      ++at;
-    }
+    place[tid] = at;
+    __syncwarp();
+    for_pages(p, b, first, last, [&](int32_t page, int64_t n, int of) {
+      const int64_t to = start - 1 - (place[32 * warp + of] + n);
+      if (to >= 0) p.free_pages[to] = page;
+    });
     __syncthreads();
   }
   if (tid == 0) {
@@ -653,6 +683,8 @@ __global__ void __launch_bounds__(kCommitThreads) commit_tree_kernel(const Commi
   const int64_t unit = (static_cast<int64_t>(blockIdx.x) - 1) * (kCommitThreads / 32) + (threadIdx.x >> 5);
   if (unit >= p.n_req * p.n_layers) return;
   const int64_t b = unit / p.n_layers, layer = unit % p.n_layers;
+  // the first entries of keep are requested beside the lengths that say how many of them count
+  int64_t from = lane < p.max_keep ? __ldg(p.keep + b * p.max_keep + lane) : -1;
   const Kept k = kept_of(p, b);
   __nv_bfloat16* pool = p.pool + layer * p.layer_stride;
   const int pieces = p.d_qk / 8;
@@ -660,7 +692,7 @@ __global__ void __launch_bounds__(kCommitThreads) commit_tree_kernel(const Commi
     const int64_t i = i0 + lane;
     int64_t src = -1, dst = -1;
     if (i < k.n) {
-      const int64_t from = __ldg(p.keep + b * p.max_keep + i);
+      if (i0 > 0) from = __ldg(p.keep + b * p.max_keep + i);
       if (from > i && from < k.n_k - k.before) {
         src = pool_row(p, b, k.before + from);
         dst = pool_row(p, b, k.before + i);
@@ -668,23 +700,25 @@ __global__ void __launch_bounds__(kCommitThreads) commit_tree_kernel(const Commi
     }
     uint32_t todo = __ballot_sync(kAll, src >= 0 && dst >= 0);
     while (todo) {
-      int64_t from[kRowsInFlight], to[kRowsInFlight];
+      int64_t row[kRowsInFlight], to[kRowsInFlight];
 #pragma unroll
       for (int x = 0; x < kRowsInFlight; ++x) {
         const int who = todo ? __ffs(todo) - 1 : 0;
-        from[x] = __shfl_sync(kAll, src, who);
+        row[x] = __shfl_sync(kAll, src, who);
         to[x] = todo ? __shfl_sync(kAll, dst, who) : -1;
         todo &= todo - 1;
       }
-      for (int c = lane; c < pieces; c += 32) {
-        uint4 v[kRowsInFlight];
+      uint4 v[3][kRowsInFlight];
+#pragma unroll
+      for (int u = 0; u < 3; ++u)
 #pragma unroll
         for (int x = 0; x < kRowsInFlight; ++x)
-          if (to[x] >= 0) v[x] = reinterpret_cast<const uint4*>(pool + from[x] * p.d_qk)[c];
+          if (to[x] >= 0 && lane + 32 * u < pieces) v[u][x] = reinterpret_cast<const uint4*>(pool + row[x] * p.d_qk)[lane + 32 * u];
+#pragma unroll
+      for (int u = 0; u < 3; ++u)
 #pragma unroll
         for (int x = 0; x < kRowsInFlight; ++x)
-          if (to[x] >= 0) reinterpret_cast<uint4*>(pool + to[x] * p.d_qk)[c] = v[x];
-      }
+          if (to[x] >= 0 && lane + 32 * u < pieces) reinterpret_cast<uint4*>(pool + to[x] * p.d_qk)[lane + 32 * u] = v[u][x];
     }
   }
 }
@@ -794,7 +828,8 @@ smla_status sparse_mla_commit_tree(const int32_t* keep, const int32_t* n_keep, i
   if (any_overlap(in, written)) return SMLA_ERR_BAD_SHAPE;
   const int64_t per_cta = kCommitThreads / 32, ctas = 1 + (n_req * n_layers + per_cta - 1) / per_cta;
   if (ctas > INT32_MAX) return SMLA_ERR_BAD_SHAPE;
-  const CommitParams p{keep, n_keep, cu_seqlens_q, seqlens_k, block_table, static_cast<__nv_bfloat16*>(kv_pool), free_pages,
+  const CommitParams p{keep, n_keep, cu_seqlens_q, seqlens_k, block_table, static_cast<__nv_bfloat16*>(kv_pool),
+                       n_free > 0 ? free_pages : nullptr,
                        free_start, seqlens, counts, n_req, n_free, layer_stride, pool_rows, max_keep, max_blocks,
                        page_block, n_layers, d_qk};
   commit_tree_kernel<<<static_cast<unsigned>(ctas), kCommitThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);

@@ -654,7 +654,7 @@ def commit_loops(keep, n_keep, cu, seqlens_k, table, pool, page, free, start):
                     pool[:, dst] = pool[:, src]
         kept += max(m, 0)
         lengths.append(0 if n_keep[b] < 0 else max(before + m, 0))
-        if free is not None:
+        if free is not None and len(free):
             for col in range(min(-(-lengths[-1] // page), width), min(-(-n_k // page), width)):
                 if table[b, col] >= 0:
                     if at > 0:
@@ -721,6 +721,13 @@ def test_commit_many_requests(n_req):
     rng = np.random.default_rng(n_req)
     commit_check(commit_case(n_req, rng.integers(0, 12, n_req).tolist(), 16, 2, 512))
     commit_check(commit_case(n_req, rng.integers(0, 3, n_req).tolist(), 4, 1, 576, old_max=400, done=0.5))
+
+
+def test_commit_long_requests_that_are_done():
+    """Requests with many pages, ended beside ones that go on; holes in their tables."""
+    rng = np.random.default_rng(0)
+    for n_req, old_max, page, holes in ((5, 3000, 4, 0.0), (70, 400, 1, 0.2), (300, 900, 8, 0.05), (33, 5 * 16, 16, 0.0)):
+        commit_check(commit_case(n_req, rng.integers(0, 9, n_req).tolist(), page, 1, 512, old_max=old_max, done=0.4, holes=holes))
 
 
 def test_commit_counts_of_every_kind():
