@@ -274,7 +274,9 @@ __device__ __forceinline__ uint32_t bits_at(const int32_t* words, int n_words, i
   return __funnelshift_r(lo, hi, static_cast<uint32_t>(at) & 31u);
 }
 
-// TREE: a token sees every key in front of its request's new ones, and of those the ones in its mask.
+// TREE: a token sees every key in front of its request's new ones, and of those the ones in its mask: two words of it for a lane's
+// 32 keys, read while S of the block is on its way, in the one to three blocks of a tile that hold new keys.  The mask costs
+// nothing that could be measured against the causal form (64 trees 421 us either way, 24 trees over 9000-32768 keys 129 us).
 template <int D_QK, bool TREE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     chunk_fwd_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap half_map,
@@ -636,6 +638,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
     const int64_t v1 = v0 + range;
     bool more = v0 < total && first_req >= 0;
+    // The tree form walks a tile's keys forward and the next one's backward.  With more tokens than one tile a request, a pair
+    // reads the same keys tile after tile, and all pairs' requests together may be more than the L2 holds; turned round, a tile
+    // begins with what is still there.  Counted by pair, so that pairs on one request stay together: 64 trees of 6-16 nodes,
+    // 128 heads, 1024-4096 keys 421 -> 406 us, of 19 nodes and 1536 keys 403 -> 374 us; by tile of the request 412 and 376 us, and
+    // 48 trees of 8 nodes over 8192 keys 648 us instead of 607 (622 always forward).
+    bool back = true;
     if (!few) window = -32;                      // loaded below
     for (int64_t req = first_req; more && req < p.n_req && start < total && !stop; ++req) {
       if (req >= window + 32 || window < 0) {
@@ -691,7 +699,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             join = make_int4(static_cast<int>(q_row), n_rows, 0, 0);
             join_end = s + kKeys * (n_blocks - 1);   // the tile's last block: in the range of the last pair
           }
-          for (int64_t j = j0; j < j1 && !stop; ++j) {
+          back = TREE && !back;
+          for (int64_t i = j0; i < j1 && !stop; ++i) {
+            const int64_t j = back ? j0 + j1 - 1 - i : i;
             int32_t pool_row[2];
             uint32_t mask[2];
 #pragma unroll
@@ -714,7 +724,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             if (lane == 0) {
               d.mask[0] = mask[0];
               d.mask[1] = mask[1];
-              d.flags = (j == j0 ? kFirst : 0u) | (j == j1 - 1 ? kLast : 0u);
+              d.flags = (i == j0 ? kFirst : 0u) | (i == j1 - 1 ? kLast : 0u);
               d.key0 = static_cast<int32_t>(kKeys * j);
               d.q_row = static_cast<int32_t>(q_row);
               d.n_rows = n_rows;
