@@ -392,7 +392,8 @@ smla_status sparse_mla_chunk_selftest_wait_timeout(uint64_t limit_ns, smla_strea
  *   tree_mask    [n_tok, mask_words] int32 (written): bit j of word w of row t is set when node 32 w + j is in A_i.
  *                Nodes from 32 mask_words on are in no mask.
  *   positions    [n_tok] int32 (written): seqlens_k[b] - n_b + |A_i| - 1, the position for the rotary columns
- * Rows of no request get an empty mask and position -1.  mask_words is 1 .. 1024.  All pointers 4-byte aligned.
+ * Rows of no request get an empty mask and position -1.  mask_words is 1 .. 1024, n_tok at most 2^30.  All pointers 4-byte
+ * aligned.
  * SMLA_ERR_BAD_SHAPE when an output overlaps an input or the other output.  n_tok == 0 is a no-op.
  */
 smla_status sparse_mla_plan_tree(const int32_t* parents, const int32_t* cu_seqlens_q, const int32_t* seqlens_k,

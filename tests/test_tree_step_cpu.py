@@ -35,7 +35,7 @@ def plan(lib, **kw):
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(n_req=-1), SHAPE), (dict(n_tok=-1), SHAPE), (dict(n_req=1 << 31), SHAPE), (dict(n_tok=1 << 31), SHAPE),
+    (dict(n_req=-1), SHAPE), (dict(n_tok=-1), SHAPE), (dict(n_req=1 << 31), SHAPE), (dict(n_tok=1 + (1 << 30)), SHAPE),
     (dict(words=0), SHAPE), (dict(words=1025), SHAPE),
     *[({n: None}, NULL) for n in PLAN], *[({n: PLAN[n] + 2}, MISALIGNED) for n in PLAN],
     (dict(mask=FAKE), SHAPE), (dict(mask=FAKE + STEP + 16), SHAPE), (dict(positions=FAKE + 2 * STEP + 12), SHAPE),

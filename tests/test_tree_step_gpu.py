@@ -75,7 +75,7 @@ def plan_tree_loops(parents, cu, seqlens_k, n_tok, words):
 @pytest.mark.parametrize("kind", ["tree", "chain", "star", "comb", "any"])
 @pytest.mark.parametrize("sizes,words,pad", [
     ([1], 1, 0), ([2], 1, 3), ([31, 32, 33], 2, 0), ([8] * 8, 1, 5), ([0, 64, 0, 65, 1, 0], 3, 2), ([700], 22, 1),
-    ([128, 1, 127, 96, 97], 4, 0), ([64, 40], 1, 0), ([200, 7], 3, 9), (None, 2, 40), ([], 1, 6), ([0, 0], 2, 4), ([30, 70], 9, 0),
+    ([128, 1, 127, 96, 97], 4, 0), ([128, 1, 127, 96, 160, 161, 33], 5, 0), ([1100, 40], 40, 3), ([64, 40], 1, 0), ([200, 7], 3, 9), (None, 2, 40), ([], 1, 6), ([0, 0], 2, 4), ([30, 70], 9, 0),
 ])
 def test_plan_tree_against_loops(kind, sizes, words, pad):
     rng = np.random.default_rng(words + pad)
