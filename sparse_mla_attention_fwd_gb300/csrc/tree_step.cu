@@ -149,10 +149,10 @@ __global__ void __launch_bounds__(32 * kPlanWarps) plan_tree_kernel(const TreePl
 //
 // What bounds it.  Large batches: DRAM.  256 chains of up to six nodes over 128000 tokens, 236 MB: 45 us, of which 37 us are
 // the rows (6.4 TB/s; 6.7 TB/s by the difference of two vocabularies) and 8 us the chain of latencies in front (sums of nodes,
-// nodes, their probabilities, the walk) and behind (exchange, search).  Small ones: that chain, 5.7 us for a request of one
-// node and 32000 tokens, and 3 us for each further pass (32 trees with up to five rejections at a node over 100003 tokens:
-// 21 us).  One CTA a request instead of a cluster: 1 chain 25 us, 32 trees 203 us.  Two steps of loads under way per warp;
-// three and four, copies through shared memory (cp.async, 4 bytes) and CTAs of 512 or 1024 threads were no faster.
+// nodes, their probabilities, the walk) and behind (exchange, search).  Small ones: that chain, 5.8 us for a request of one
+// node and 32000 tokens, and 2 to 3 us for each further pass (32 trees with up to five rejections at a node over 100003
+// tokens: 19 us).  One CTA a request instead of a cluster: 1 chain 25 us, 32 trees 203 us.  No faster: 16 CTAs a cluster,
+// copies through shared memory (cp.async, 4 bytes), CTAs of 512 or 1024 threads, the warps' sums sent without the CTA's.
 constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kMaxCluster = 8;
@@ -258,19 +258,19 @@ struct Step {
   }
 };
 
-// Sums of r over the tiles of [v0, v1), tile values each (a multiple of 256), into sums[0], sums[1], ..; a warp.  Two steps' loads
-// are under way, and four sums a lane are added to in turn.
-template <bool DRAFT, bool WIDE>
+// Sums of r over the tiles of [v0, v1), tile values each (a multiple of 128 STEPS), into sums[0], sums[1], ..; a warp.
+// STEPS steps' loads are under way, and four sums a lane are added to in turn.
+template <bool DRAFT, bool WIDE, int STEPS>
 __device__ __forceinline__ void tile_sums(const Residual& r, int v0, int v1, int tile, Sum* sums) {
   const int lane = threadIdx.x & 31;
-  Step<DRAFT, WIDE> step[2];
-  step[0].load(r, v0, v1);
-  step[1].load(r, v0 + 128, v1);
+  Step<DRAFT, WIDE> step[STEPS];
+#pragma unroll
+  for (int k = 0; k < STEPS; ++k) step[k].load(r, v0 + 128 * k, v1);
   for (int a = v0; a < v1; a += tile, ++sums) {
     const int end = min(a + tile, v1);
     Sum part[4] = {};
     uint32_t skip = 0;                 // this lane's values of 1024 that are gone: bit 4 step + u
-    for (int v = a; v < end; v += 256) {
+    for (int v = a; v < end; v += 128 * STEPS) {
       if (!DRAFT && ((v - a) & 1023) == 0) {
         skip = 0;
         for (int i = 0; i < r.n_gone; ++i) {
@@ -279,7 +279,7 @@ __device__ __forceinline__ void tile_sums(const Residual& r, int v0, int v1, int
         }
       }
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+      for (int k = 0; k < STEPS; ++k) {
         float x[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -287,7 +287,7 @@ __device__ __forceinline__ void tile_sums(const Residual& r, int v0, int v1, int
           if (!DRAFT && (skip >> u & 1)) x[u] = 0.f;
         }
         skip >>= 4;
-        step[k].load(r, v + 256 + 128 * k, v1);
+        step[k].load(r, v + 128 * (STEPS + k), v1);
 #pragma unroll
         for (int u = 0; u < 4; ++u) part[u].add(x[u]);
       }
@@ -349,7 +349,8 @@ __device__ __forceinline__ void load_nodes(const VerifyParams& p, const NodeRang
   }
 }
 
-__global__ void __launch_bounds__(kVerifyThreads, 4) verify_tree_kernel(const VerifyParams p) {
+template <int STEPS>
+__global__ void __launch_bounds__(kVerifyThreads, 8 / STEPS) verify_tree_kernel(const VerifyParams p) {
   __shared__ VerifyShared s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = static_cast<int>(cluster_rank()), ranks = static_cast<int>(cluster_size());
@@ -458,25 +459,25 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_tree_kernel(const Ve
     const int v0 = min(first + warp * mine * p.tile, behind), v1 = min(v0 + mine * p.tile, behind);
     Sum* sums = s.sums + warp * mine;
     if (wide) {
-      if (left.q) tile_sums<true, true>(left, v0, v1, p.tile, sums);
-      else tile_sums<false, true>(left, v0, v1, p.tile, sums);
+      if (left.q) tile_sums<true, true, STEPS>(left, v0, v1, p.tile, sums);
+      else tile_sums<false, true, STEPS>(left, v0, v1, p.tile, sums);
     } else {
-      if (left.q) tile_sums<true, false>(left, v0, v1, p.tile, sums);
-      else tile_sums<false, false>(left, v0, v1, p.tile, sums);
+      if (left.q) tile_sums<true, false, STEPS>(left, v0, v1, p.tile, sums);
+      else tile_sums<false, false, STEPS>(left, v0, v1, p.tile, sums);
     }
     __syncthreads();
     if (pass == 0) cluster_wait();
+    const Sum* totals = s.totals[pass & 1];
     if (warp == 0) {
       Sum sum{0.f, 0.f};
       for (int i = lane; i < tiles; i += 32) sum.add(s.sums[i]);
       add_lanes(sum);
-      if (lane < ranks) store_floats(map_to_rank(smem_u32(&s.totals[pass & 1][rank]), lane), sum.hi, sum.lo);
+      if (lane < ranks) store_floats(map_to_rank(smem_u32(totals + rank), lane), sum.hi, sum.lo);
       __syncwarp();
     }
     cluster_arrive();
     cluster_wait();
     if (warp == 0) {
-      const Sum* totals = s.totals[pass & 1];
       Sum sum = lane < ranks ? totals[lane] : Sum{0.f, 0.f};
       add_lanes(sum);
       int then = kWalkOn;
@@ -810,14 +811,18 @@ smla_status sparse_mla_verify_tree(const float* target_probs, int64_t target_str
   if (any_overlap(in, written)) return SMLA_ERR_BAD_SHAPE;
   VerifyParams p{target_probs, draft_probs, tokens, parents, cu_seqlens_q, accept_u, sample_u, keep, out_tokens,
                        n_keep, target_stride, draft_stride, n_req, n_tok, vocab, max_keep, 0, 0};
-  // A cluster of up to eight CTAs, while there is work for each and all clusters run at once (four CTAs an SM)
+  // A cluster of up to eight CTAs, while there is work for each and all clusters run at once (four CTAs an SM): 256 chains 45 us
+  // with two, 50 with four, 57 with eight CTAs; 100 chains 31, 23.5, 29; 60 chains 29, 19, 15; 1 chain 8.5, 7.4, 6.9.
   int ranks = 1;
   while (ranks < kMaxCluster && vocab > ranks * kTile && n_req * ranks * 2 <= 4 * 152) ranks *= 2;
+  // Four steps of loads under way where two CTAs an SM are enough, else two: 32 trees over 100003 tokens (256 CTAs) 19.0 and
+  // 21.0 us, 48 over 50001 (384 CTAs) 13.2 and 10.1, 256 chains 51 and 45.
+  const int steps = n_req * ranks <= 2 * 152 ? 4 : 2;
   p.each = ((vocab + 3 + ranks - 1) / ranks + 3) / 4 * 4;
   p.tile = (p.each + kVerifyWarps - 1) / kVerifyWarps;
   p.tile = p.tile > kTile ? kTile : p.tile;
   if (p.each > p.tile * kMaxTiles) p.tile = (p.each + kMaxTiles - 1) / kMaxTiles;
-  p.tile = (p.tile + 255) / 256 * 256;
+  p.tile = (p.tile + 128 * steps - 1) / (128 * steps) * (128 * steps);
   cudaLaunchAttribute cluster{};
   cluster.id = cudaLaunchAttributeClusterDimension;
   cluster.val.clusterDim.x = ranks;
@@ -829,7 +834,8 @@ smla_status sparse_mla_verify_tree(const float* target_probs, int64_t target_str
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
   cfg.attrs = &cluster;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, verify_tree_kernel, p) == cudaSuccess ? SMLA_OK : SMLA_ERR_LAUNCH;
+  const auto kernel = steps == 4 ? verify_tree_kernel<4> : verify_tree_kernel<2>;
+  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? SMLA_OK : SMLA_ERR_LAUNCH;
 }
 
 smla_status sparse_mla_commit_tree(const int32_t* keep, const int32_t* n_keep, int max_keep, const int32_t* cu_seqlens_q,
