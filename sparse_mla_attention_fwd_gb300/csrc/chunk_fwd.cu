@@ -36,6 +36,10 @@
 // finished there; parts of a cut tile go to the workspace (at most two per pair) and a second
 // kernel joins them.  Nothing depends on timing, so results are the same bits from call to call.
 //
+// The same kernel attends for trees of drafted tokens (TREE): a token sees all keys in front of its request's new ones, and the
+// new ones that its row of a bit mask names.  There the axis is that of the form without causality, and four neighbouring pairs
+// share their ranges tile by tile.
+//
 // What bounds it.  A block takes 1412 cycles of the tensor unit at full rate (36 products of N = 64, which the
 // operands' 3 KB at 128 bytes a cycle of shared memory hold at 25 cycles instead of 16, and 8 of N = 256 at 64).
 // Arriving keys (52 KB) and P want the same shared memory: 1690 cycles if nothing ran beside the products.  The
@@ -82,6 +86,7 @@ constexpr int kMaxPairs = 80;             // ranges the axis is cut into, at mos
 // pair between a cut tile's ends has a part of it.
 constexpr int kTileCost = 192;
 constexpr int kMinRange = 256;
+constexpr int kTreeGroup = 4;             // neighbouring pairs that share a range in the tree form
 constexpr uint32_t kHalfBytes = 16384;    // 32 keys x 256 columns
 constexpr uint32_t kPBytes = 8192;        // 64 rows x 64 keys
 constexpr uint32_t kTmemCols = 512, kTmemS = 256;
@@ -108,7 +113,7 @@ struct ChunkParams {
   float* max_logits;
   float* part_o;            // [2 pairs][128 column quads][row_cap][4] unnormalised O of a tile's part
   float* part_stats;        // [2 pairs][3][128]: offset (log2 units), sum, maximum score
-  int4* joins;              // [pairs]: first row, rows, last pair of the cut tile that starts there
+  int4* joins;              // [pairs]: first row, rows, last pair of the cut tile that starts there, pairs behind it without a part (bits)
   int64_t pool_rows, n_req, n_tok;
   float sm_scale;
   int h_q, max_blocks, page_block, causal;
@@ -294,6 +299,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const uint32_t rank = cluster_rank();
   const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int64_t first_pair = TREE ? pair / kTreeGroup * kTreeGroup : pair;   // of those that share a range
   volatile int* abort = &c.abort_flag;
 
   if (tid == 0) {
@@ -338,7 +344,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const int64_t upto = pair_scan(mine, scan.warp_sum);
     if (tid == kPairThreads - 1) scan.total = scan.run = upto;
     __syncthreads();
-    const int64_t v0 = pair * range_of(scan.total, pairs);
+    const int64_t v0 = first_pair * range_of(scan.total, pairs);
     if (p.n_req <= kPairThreads) {
       if (upto - mine <= v0 && v0 < upto) {
         scan.req = tid;
@@ -605,7 +611,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       ++b;
     };
     int4 join = make_int4(0, 0, -1, 0);
-    int64_t join_end = 0;
+    int64_t join_end = 0, join_start = 0;
     const bool few = p.n_req <= 32;
     Request mine{};                              // of request `window` + lane
     int64_t window = 0;
@@ -625,24 +631,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       }
       total = __shfl_sync(0xffffffffu, end, 31);
       range = range_of(total, pairs);
-      v0 = pair * range;
+      v0 = first_pair * range;
       const uint32_t hit = __ballot_sync(0xffffffffu, end - cost <= v0 && v0 < end);
       first_req = __ffs(hit) - 1;                // -1: the range lies behind the axis' end
       start = __shfl_sync(0xffffffffu, end - cost, hit ? __ffs(hit) - 1 : 0);
     } else {
       total = scan.total;
       range = range_of(total, pairs);
-      v0 = pair * range;
+      v0 = first_pair * range;
       first_req = scan.req;
       start = scan.start;
     }
-    const int64_t v1 = v0 + range;
+    const int64_t members = TREE ? min(static_cast<int64_t>(kTreeGroup), pairs - first_pair) : 1;
+    const int64_t v1 = v0 + members * range;
+    // TREE: the pairs that share a range take its tiles in turn, each tile to the least loaded one, as long as it fits; what is then
+    // left of the range goes to them in pieces, in order: [a, e) to this one.  A tile longer than a pair's share is cut as in
+    // the causal form, and there are no more cuts than there.
+    int64_t load[kTreeGroup], a = v0, e = v1;
+#pragma unroll
+    for (int g = 0; g < kTreeGroup; ++g) load[g] = g < members ? 0 : range;
+    bool pieces = !TREE;
     bool more = v0 < total && first_req >= 0;
-    // The tree form walks a tile's keys forward and the next one's backward.  With more tokens than one tile a request, a pair
-    // reads the same keys tile after tile, and all pairs' requests together may be more than the L2 holds; turned round, a tile
-    // begins with what is still there.  Counted by pair, so that pairs on one request stay together: 64 trees of 6-16 nodes,
-    // 128 heads, 1024-4096 keys 421 -> 406 us, of 19 nodes and 1536 keys 403 -> 374 us; by tile of the request 412 and 376 us, and
-    // 48 trees of 8 nodes over 8192 keys 648 us instead of 607 (622 always forward).
+    // The tree form has several tiles on one request's keys, one after the other, and all requests' keys together may be more
+    // than the L2 holds.  So four neighbouring pairs share a range and take its tiles in turn (above), and each walks one tile's
+    // keys forward and its next one's backward, which begins with what is still there.  64 trees of 6-16 nodes, 128 heads,
+    // 1024-4096 keys: 1.6 GB from DRAM without the sharing, 0.6 with it; alone and forward 421 us, alone in turns 406, by four in
+    // turns 399 (over seconds, at the power limit: 474, 454, 428); 64 of 19 nodes over 2560 keys 635, 613, 592 (731, 690, 643).
+    // Keys that fit the L2 gain nothing (16 trees of 19 nodes over 10240: 565, 560, 565).  By two pairs 398 and 594 us, but 48
+    // trees of 8 nodes over 8192 keys 629 instead of 601; by eight 432: too many ask for the same rows at once.
     bool back = true;
     if (!few) window = -32;                      // loaded below
     for (int64_t req = first_req; more && req < p.n_req && start < total && !stop; ++req) {
@@ -683,12 +699,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         const int64_t key_end = p.causal ? min(max(before + last, static_cast<int64_t>(0)), r.keys) : r.keys;
         const int64_t n_blocks = max((key_end + kKeys - 1) / kKeys, static_cast<int64_t>(1));
         for (int grp = 0; grp < p.groups && more && !stop; ++grp, s += size) {
-          if (s >= v1) {
+          if (s >= e) {
             more = false;
             break;
           }
-          const int64_t j0 = s >= v0 ? 0 : (v0 - s + kKeys - 1) / kKeys;
-          const int64_t j1 = min(n_blocks, (v1 - s + kKeys - 1) / kKeys);
+          if (!pieces) {
+            if (s + size <= v0) continue;        // another group of heads of the token in which the range starts
+            const int64_t begin = max(s, v0), len = s + size - begin;
+            int to = 0;
+            int64_t least = load[0];
+#pragma unroll
+            for (int g = 1; g < kTreeGroup; ++g)
+              if (load[g] < least) {
+                least = load[g];
+                to = g;
+              }
+            if (s + size <= v1 && least + len <= range) {
+#pragma unroll
+              for (int g = 0; g < kTreeGroup; ++g) load[g] += g == to ? len : 0;
+              if (first_pair + to != pair) continue;
+            } else {
+              pieces = true;
+              e = begin;
+#pragma unroll
+              for (int g = 0; g < kTreeGroup; ++g)
+                if (first_pair + g <= pair) {
+                  a = e;
+                  e += range - load[g];
+                }
+              if (s >= e) {
+                more = false;
+                break;
+              }
+            }
+          }
+          const int64_t j0 = s >= a ? 0 : (a - s + kKeys - 1) / kKeys;
+          const int64_t j1 = min(n_blocks, (e - s + kKeys - 1) / kKeys);
           if (j0 >= j1) continue;
           const int64_t q_row = (r.q0 + tok) * p.h_q + (p.groups > 1 ? kTileRows * grp : 0);
           const int n_rows = p.groups > 1 ? min(kTileRows, p.h_q - kTileRows * grp) : static_cast<int>(last - tok) * p.h_q;
@@ -698,6 +744,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             part = static_cast<int>(2 * pair + 1);
             join = make_int4(static_cast<int>(q_row), n_rows, 0, 0);
             join_end = s + kKeys * (n_blocks - 1);   // the tile's last block: in the range of the last pair
+            join_start = s;
           }
           back = TREE && !back;
           for (int64_t i = j0; i < j1 && !stop; ++i) {
@@ -738,7 +785,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       }
       start = s;
     }
-    if (join.z == 0) join.z = static_cast<int>(join_end / range);
+    if (join.z == 0) {   // the pair that has the cut tile's last block, and (w) which ones in between have none of it
+      join.z = static_cast<int>(join_end / range);
+      if (TREE) {
+        if (join_end < e) join.z = static_cast<int>(pair);
+        int64_t begin = e;
+#pragma unroll
+        for (int g = 1; g < kTreeGroup; ++g)
+          if (first_pair + g > pair && begin <= join_end) {
+            const int64_t end = begin + range - load[g];
+            if (join_end < v1) join.z = static_cast<int>(first_pair + g);
+            if ((begin - join_start + kKeys - 1) / kKeys == (end - join_start + kKeys - 1) / kKeys) join.w |= 1 << (first_pair + g - pair);
+            begin = end;
+          }
+      }
+    }
     acquire();
     if (lane == 0) {
       c.ring[b % kRing].flags = kEnd;
@@ -945,11 +1006,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) chunk_join_kernel(const Chunk
     for (int u = 0; u < kJoinParts; ++u) {
       const int i = min(i0 + u, join.z), slot = i == w ? 2 * w + 1 : 2 * i;
       const float* st = stats + slot * 3 * 128;
-      m[u] = st[0];
-      li[u] = st[128];
-      ti[u] = st[256];
+      const bool none = i - w < 32 && (join.w >> (i - w)) & 1;
+      m[u] = none ? -INFINITY : st[0];
+      li[u] = none ? 0.f : st[128];
+      ti[u] = none ? -INFINITY : st[256];
 #pragma unroll
-      for (int x = 0; x < 2; ++x) o[u][x] = part[(static_cast<int64_t>(slot) * 128 + x) * p.row_cap];
+      for (int x = 0; x < 2; ++x)
+        o[u][x] = none ? float4{} : part[(static_cast<int64_t>(slot) * 128 + x) * p.row_cap];
     }
     float now = M;
 #pragma unroll
