@@ -276,6 +276,28 @@ def test_tree_causal_masks_are_the_causal_form():
         assert float((out.float() - o2.float()).norm()) <= 2 * 1.5 * U16 * float(o2.float().norm())
 
 
+def test_tree_full_masks_are_the_form_without_causality():
+    """Random shapes, from one worker's to all workers' at once: the same set of keys, cut and joined another way."""
+    rng = np.random.default_rng(11)
+    for i in range(40):
+        heads, page = int(rng.choice([1, 8, 16, 20, 64, 128, 160, 512])), int(rng.choice([16, 32, 64]))
+        n_req = int(rng.choice([1, 2, 5, 33, 80]))
+        q_lens = rng.integers(0, int(rng.choice([2, 9, 33])) + 1, n_req).tolist()
+        k_lens = [q + int(10 ** rng.uniform(0, 3.6 if n_req > 5 else 4.2)) for q in q_lens]
+        while sum(q_lens) * heads > 60000:
+            q_lens = [q // 2 for q in q_lens]
+        w = chunk_case(i, q_lens, k_lens, heads, int(rng.choice([512, 576])), page=page, tail=1)
+        sink = torch.randn(heads, device="cuda") if i % 3 == 0 else None
+        n = sum(q_lens)
+        mask = torch.full((n + 1, max(1, -(-max([*q_lens, 1]) // 32))), -1, dtype=torch.int32, device="cuda")
+        a = smla.sparse_mla_tree_fwd_paged(**w, tree_mask=mask, attn_sink=sink)
+        b = smla.sparse_mla_chunk_fwd_paged(**w, causal=False, attn_sink=sink)
+        if n:
+            # the scores are the same; the sums' order and the exponents' offsets are not
+            assert torch.equal(a[2][:n], b[2][:n]) and float((a[1][:n] - b[1][:n]).abs().max()) <= 1e-4, i
+            assert float((a[0][:n].float() - b[0][:n].float()).norm()) <= 2 * 1.5 * U16 * float(b[0][:n].float().norm()), i
+
+
 def test_tree_pool_past_2_gib():
     rows = 2_500_032
     pool = torch.empty(rows, 1, 576, device="cuda", dtype=torch.bfloat16).normal_()
@@ -627,6 +649,8 @@ def test_verify_of_no_requests_and_no_nodes():
     w = verify_case(19, [0, 0], 20, pad=2)
     keep, out, n_keep = smla.sparse_mla_verify_tree(**w)
     assert keep.tolist() == [[-1], [-1]] and out.tolist() == [[-1], [-1]] and n_keep.tolist() == [0, 0]
+    empty = dict(w, **{k: w[k][:0] for k in ("target_probs", "draft_probs", "tokens", "parents", "accept_u")})
+    assert [x.tolist() for x in smla.sparse_mla_verify_tree(**empty)] == [[[-1], [-1]], [[-1], [-1]], [0, 0]]
     none = smla.sparse_mla_verify_tree(**dict(w, cu_seqlens_q=i32([0]), sample_u=w["sample_u"][:0]))
     assert [tuple(x.shape) for x in none] == [(0, 1), (0, 1), (0,)]
 
