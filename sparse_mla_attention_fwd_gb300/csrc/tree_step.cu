@@ -151,8 +151,9 @@ __global__ void __launch_bounds__(32 * kPlanWarps) plan_tree_kernel(const TreePl
 // the rows (6.4 TB/s; 6.7 TB/s by the difference of two vocabularies) and 8 us the chain of latencies in front (sums of nodes,
 // nodes, their probabilities, the walk) and behind (exchange, search).  Small ones: that chain, 5.8 us for a request of one
 // node and 32000 tokens, and 2 to 3 us for each further pass (32 trees with up to five rejections at a node over 100003
-// tokens: 19 us).  One CTA a request instead of a cluster: 1 chain 25 us, 32 trees 203 us.  No faster: 16 CTAs a cluster,
-// copies through shared memory (cp.async, 4 bytes), CTAs of 512 or 1024 threads, the warps' sums sent without the CTA's.
+// tokens: 19 us).  The first form, one CTA a request and 64-bit sums: 1 chain 25 us, 256 chains 162, 32 trees 203.  No faster:
+// 16 CTAs a cluster, copies through shared memory (cp.async, 4 bytes), CTAs of 512 or 1024 threads, the warps' sums sent
+// without the CTA's.
 constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kMaxCluster = 8;
@@ -811,13 +812,22 @@ smla_status sparse_mla_verify_tree(const float* target_probs, int64_t target_str
   if (any_overlap(in, written)) return SMLA_ERR_BAD_SHAPE;
   VerifyParams p{target_probs, draft_probs, tokens, parents, cu_seqlens_q, accept_u, sample_u, keep, out_tokens,
                        n_keep, target_stride, draft_stride, n_req, n_tok, vocab, max_keep, 0, 0};
-  // A cluster of up to eight CTAs, while there is work for each and all clusters run at once (four CTAs an SM): 256 chains 45 us
-  // with two, 50 with four, 57 with eight CTAs; 100 chains 31, 23.5, 29; 60 chains 29, 19, 15; 1 chain 8.5, 7.4, 6.9.
-  int ranks = 1;
-  while (ranks < kMaxCluster && vocab > ranks * kTile && n_req * ranks * 2 <= 4 * 152) ranks *= 2;
-  // Four steps of loads under way where two CTAs an SM are enough, else two: 32 trees over 100003 tokens (256 CTAs) 19.0 and
-  // 21.0 us, 48 over 50001 (384 CTAs) 13.2 and 10.1, 256 chains 51 and 45.
-  const int steps = n_req * ranks <= 2 * 152 ? 4 : 2;
+  // CTAs a request, and steps of loads under way.  With four steps an SM holds two CTAs, with two four; clusters of four and more
+  // do not fill the GPU to the last place, and what does not fit runs after the rest.  Over 128000 tokens, in us: 76 requests
+  // 20 (4 CTAs, 2 steps), 21 (2, 4), 24 (4 or 8, which just do not fit); 128 requests 26.0 (2, 4), 26.1 (4, 2), 32 (2, 2);
+  // 152 requests 28 (2, 4), 34 (2, 2), 38 (4, 2); 180 requests 35 (2, 2), 37 (1, 4); 256 requests 42.7 (1, 4), 42.8 (2, 2), 55 (1, 2);
+  // 400 requests 63 (1, 2), 70 (2, 2), 74 (1, 4); one request over 32000 tokens 6.7 (8), 7.4 (4), 8.5 (2), 10.8 (1).
+  constexpr int kPlaces = 2 * 152;
+  int ranks = 1, steps = 2;
+  if (n_req <= kPlaces) {
+    steps = 4;
+    const auto room = [&] { return ranks < kMaxCluster && vocab > ranks * kTile; };
+    while (room() && 2 * ranks * n_req <= (ranks == 1 ? kPlaces : kPlaces - 16)) ranks *= 2;
+    if (room() && ranks * n_req <= 3 * kPlaces / 4) {
+      ranks *= 2;
+      steps = 2;
+    }
+  }
   p.each = ((vocab + 3 + ranks - 1) / ranks + 3) / 4 * 4;
   p.tile = (p.each + kVerifyWarps - 1) / kVerifyWarps;
   p.tile = p.tile > kTile ? kTile : p.tile;
