@@ -66,6 +66,7 @@ def _stream_handle(stream, device):
 # the current stream's handle on a device; a stream object in between costs two microseconds
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_INT32_MAX = 2 ** 31 - 1
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 # torch.empty on the current device without its argument parsing, which is nearly half of its 1.5 microseconds
 try:
@@ -705,8 +706,8 @@ def sparse_mla_tree_fwd_paged(q, kv_pool, block_table, cu_seqlens_q, seqlens_k, 
     if not _ready(index, torch.int32, tree_mask):
         _dense(tree_mask, "tree_mask", torch.int32, q.device)
     mask_shape = tree_mask.shape
-    if len(mask_shape) != 2 or mask_shape[0] != n_tok:
-        raise ValueError("tree_mask must be [n_tok, words]")
+    if len(mask_shape) != 2 or mask_shape[0] != n_tok or not 0 < mask_shape[1] <= 1024:
+        raise ValueError("tree_mask must be [n_tok, words], 1 to 1024 words")
     rc = lib.sparse_mla_tree_fwd_paged(
         q.data_ptr(), kv_pool.data_ptr(), pool_rows, block_table.data_ptr(), max_blocks, int(page_block),
         cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), n_req, tree_mask.data_ptr(), mask_shape[1], _ptr(attn_sink),
@@ -721,12 +722,12 @@ def _probs(t, name, n_tok, vocab, index):
     """The row stride of an fp32 tensor [n_tok, vocab] whose last dimension is contiguous, and its vocab (any, if given as 0)."""
     if isinstance(t, torch.Tensor) and t.dtype is torch.float32 and t.get_device() == index:
         shape = t.shape
-        if len(shape) == 2 and shape[0] == n_tok and shape[1] > 0 and (shape[1] == vocab or not vocab):
+        if len(shape) == 2 and shape[0] == n_tok and 0 < shape[1] <= 1 << 30 and (shape[1] == vocab or not vocab):
             strides = t.stride()
             if strides[1] == 1 or shape[1] == 1 or n_tok == 0:
                 return strides[0], shape[1]
             raise ValueError(f"{name} must be contiguous in its last dimension")
-        raise ValueError(f"{name} must be [{n_tok}, {vocab or 'vocab'}], got {list(shape)}")
+        raise ValueError(f"{name} must be [{n_tok}, {vocab or 'vocab'}] with vocab 1 to 2^30, got {list(shape)}")
     if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32:
         raise TypeError(f"{name} must be a torch.float32 tensor")
     raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
@@ -760,8 +761,8 @@ def sparse_mla_verify_tree(target_probs, tokens, parents, cu_seqlens_q, accept_u
         raise ValueError("parents and accept_u must have one entry per token")
     if cu_seqlens_q.numel() != n_req + 1:
         raise ValueError("cu_seqlens_q must have one entry more than sample_u")
-    if max_keep < 1:
-        raise ValueError("max_keep must be at least 1")
+    if not 0 < max_keep <= _INT32_MAX // max(n_req, 1):
+        raise ValueError("max_keep must be at least 1, and n_req * max_keep fit 31 bits")
     t_stride, vocab = _probs(target_probs, "target_probs", n_tok, 0, index)
     d_stride, draft = 0, None
     if draft_probs is not None:
@@ -828,7 +829,7 @@ def sparse_mla_commit_tree(keep, n_keep, cu_seqlens_q, seqlens_k, block_table, k
         _dense(seqlens_k, "seqlens_k", i32, dev)
         _dense(block_table, "block_table", i32, dev)
     n_req, keep_shape, table_shape = seqlens_k.numel(), keep.shape, block_table.shape
-    if len(keep_shape) != 2 or keep_shape[0] != n_req or keep_shape[1] < 1 or n_keep.numel() != n_req:
+    if len(keep_shape) != 2 or keep_shape[0] != n_req or not 0 < keep_shape[1] <= _INT32_MAX or n_keep.numel() != n_req:
         raise ValueError("keep must be [n_req, max_keep] and n_keep have n_req entries")
     if cu_seqlens_q.numel() != n_req + 1:
         raise ValueError("cu_seqlens_q must have n_req + 1 entries")

@@ -811,7 +811,7 @@ smla_status sparse_mla_verify_tree(const float* target_probs, int64_t target_str
   const Span written[] = {{keep, reqs * max_keep}, {out_tokens, reqs * max_keep}, {n_keep, reqs}};
   if (any_overlap(in, written)) return SMLA_ERR_BAD_SHAPE;
   VerifyParams p{target_probs, draft_probs, tokens, parents, cu_seqlens_q, accept_u, sample_u, keep, out_tokens,
-                       n_keep, target_stride, draft_stride, n_req, n_tok, vocab, max_keep, 0, 0};
+                 n_keep, target_stride, draft_stride, n_req, n_tok, vocab, max_keep, 0, 0};
   // CTAs a request, and steps of loads under way.  With four steps an SM holds two CTAs, with two four; clusters of four and more
   // do not fill the GPU to the last place, and what does not fit runs after the rest.  Over 128000 tokens, in us: 76 requests
   // 20 (4 CTAs, 2 steps), 21 (2, 4), 24 (4 or 8, which just do not fit); 128 requests 26.0 (2, 4), 26.1 (4, 2), 32 (2, 2);
