@@ -270,24 +270,21 @@ __device__ __forceinline__ void tile_sums(const Residual& r, int v0, int v1, int
   for (int a = v0; a < v1; a += tile, ++sums) {
     const int end = min(a + tile, v1);
     Sum part[4] = {};
-    uint32_t skip = 0;                 // this lane's values of 1024 that are gone: bit 4 step + u
     for (int v = a; v < end; v += 128 * STEPS) {
-      if (!DRAFT && ((v - a) & 1023) == 0) {
-        skip = 0;
+      uint32_t skip = 0;               // this lane's values that are gone: bit 4 step + u
+      if (!DRAFT)
         for (int i = 0; i < r.n_gone; ++i) {
           const uint32_t d = static_cast<uint32_t>(r.gone[i] - v);
-          if (d < 1024u && (WIDE ? (d >> 2) & 31 : d & 31) == lane) skip |= 1u << (((d >> 7) << 2) + (WIDE ? d & 3 : (d >> 5) & 3));
+          if (d < 128u * STEPS && (WIDE ? (d >> 2) & 31 : d & 31) == lane) skip |= 1u << (((d >> 7) << 2) + (WIDE ? d & 3 : (d >> 5) & 3));
         }
-      }
 #pragma unroll
       for (int k = 0; k < STEPS; ++k) {
         float x[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           x[u] = fmaxf(DRAFT ? fmaf(-r.c, step[k].q[DRAFT ? u : 0], step[k].p[u]) : step[k].p[u], 0.f);
-          if (!DRAFT && (skip >> u & 1)) x[u] = 0.f;
+          if (!DRAFT && (skip >> (4 * k + u) & 1)) x[u] = 0.f;
         }
-        skip >>= 4;
         step[k].load(r, v + 128 * (STEPS + k), v1);
 #pragma unroll
         for (int u = 0; u < 4; ++u) part[u].add(x[u]);
@@ -351,7 +348,7 @@ __device__ __forceinline__ void load_nodes(const VerifyParams& p, const NodeRang
 }
 
 template <int STEPS>
-__global__ void __launch_bounds__(kVerifyThreads, 8 / STEPS) verify_tree_kernel(const VerifyParams p) {
+__global__ void __launch_bounds__(kVerifyThreads, STEPS == 4 ? 2 : STEPS == 3 ? 3 : 4) verify_tree_kernel(const VerifyParams p) {
   __shared__ VerifyShared s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = static_cast<int>(cluster_rank()), ranks = static_cast<int>(cluster_size());
@@ -812,25 +809,28 @@ smla_status sparse_mla_verify_tree(const float* target_probs, int64_t target_str
   if (any_overlap(in, written)) return SMLA_ERR_BAD_SHAPE;
   VerifyParams p{target_probs, draft_probs, tokens, parents, cu_seqlens_q, accept_u, sample_u, keep, out_tokens,
                  n_keep, target_stride, draft_stride, n_req, n_tok, vocab, max_keep, 0, 0};
-  // CTAs a request, and steps of loads under way.  With four steps an SM holds two CTAs, with two four; clusters of four and more
-  // do not fill the GPU to the last place, and what does not fit runs after the rest.  Over 128000 tokens, in us: 76 requests
-  // 20 (4 CTAs, 2 steps), 21 (2, 4), 24 (4 or 8, which just do not fit); 128 requests 26.0 (2, 4), 26.1 (4, 2), 32 (2, 2);
-  // 152 requests 28 (2, 4), 34 (2, 2), 38 (4, 2); 180 requests 35 (2, 2), 37 (1, 4); 256 requests 42.7 (1, 4), 42.8 (2, 2), 55 (1, 2);
-  // 400 requests 63 (1, 2), 70 (2, 2), 74 (1, 4); one request over 32000 tokens 6.7 (8), 7.4 (4), 8.5 (2), 10.8 (1).
-  constexpr int kPlaces = 2 * 152;
-  int ranks = 1, steps = 2;
-  if (n_req <= kPlaces) {
-    steps = 4;
-    const auto room = [&] { return ranks < kMaxCluster && vocab > ranks * kTile; };
-    while (room() && 2 * ranks * n_req <= (ranks == 1 ? kPlaces : kPlaces - 16)) ranks *= 2;
-    if (room() && ranks * n_req <= 3 * kPlaces / 4) {
+  // CTAs a request, and steps of loads under way: four where two CTAs an SM are enough, three for three, two for four.  Clusters of
+  // four and more do not fill the GPU to the last place, and what does not fit runs after the rest.  Over 128000 tokens, in us,
+  // (CTAs, steps): 48 requests 11.7 (8, 3), 12.6 (8, 2), 12.8 (4, 4); 76 requests 20 (4, 2), 21 (2, 4), 24 (4, 4), which just does not
+  // fit; 128 requests 26.0 (2, 4), 26.1 (4, 2); 152 requests 28 (2, 4), 34 (2, 2), 38 (4, 2); 200 requests 33 (2, 3), 36 (2, 2), 38 (1, 4);
+  // 256 requests 41.6 (1, 4), 42.0 (2, 2), 45 (1, 3), 54 (1, 2); 400 requests 59 (1, 3), 63 (1, 2), 74 (1, 4); 512 requests 72 (1, 2),
+  // 79 (1, 4), 93 (1, 3).  One request over 32000 tokens 6.7 (8), 7.4 (4), 8.5 (2), 10.8 (1).
+  const auto fits = [&](int r, int steps) {
+    return r * n_req <= 152 * (steps == 4 ? 2 : steps == 3 ? 3 : 4) - (r < 4 ? 0 : r == 4 || steps == 4 ? 16 : 64);
+  };
+  const auto room = [&](int r) { return r < kMaxCluster && vocab > r * kTile; };
+  int ranks = 1, steps = fits(1, 4) ? 4 : fits(1, 3) ? 3 : 2;
+  if (steps == 4) {
+    while (room(ranks) && fits(2 * ranks, 4)) ranks *= 2;
+    if (room(ranks) && ranks * n_req <= 3 * 152 / 2) {
       ranks *= 2;
-      steps = 2;
+      steps = fits(ranks, 3) ? 3 : 2;
     }
   }
   p.each = ((vocab + 3 + ranks - 1) / ranks + 3) / 4 * 4;
   p.tile = (p.each + kVerifyWarps - 1) / kVerifyWarps;
-  p.tile = p.tile > kTile ? kTile : p.tile;
+  const int most = kTile / (128 * steps) * (128 * steps);
+  p.tile = p.tile > most ? most : p.tile;
   if (p.each > p.tile * kMaxTiles) p.tile = (p.each + kMaxTiles - 1) / kMaxTiles;
   p.tile = (p.tile + 128 * steps - 1) / (128 * steps) * (128 * steps);
   cudaLaunchAttribute cluster{};
@@ -844,7 +844,7 @@ smla_status sparse_mla_verify_tree(const float* target_probs, int64_t target_str
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
   cfg.attrs = &cluster;
   cfg.numAttrs = 1;
-  const auto kernel = steps == 4 ? verify_tree_kernel<4> : verify_tree_kernel<2>;
+  const auto kernel = steps == 4 ? verify_tree_kernel<4> : steps == 3 ? verify_tree_kernel<3> : verify_tree_kernel<2>;
   return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? SMLA_OK : SMLA_ERR_LAUNCH;
 }
 
