@@ -407,7 +407,8 @@ smla_status sparse_mla_plan_tree(const int32_t* parents, const int32_t* cu_seqle
  *   tree_mask     [n_tok, mask_words] int32, mask_words 1 .. 1024; nodes from 32 mask_words on are seen by none
  * Everything else is as there: ragged requests, page rules, workspace (sparse_mla_chunk_workspace_size), empty
  * rows (a node that sees nothing: O = 0, lse = +inf, max_logits = -inf), NaN, rows that are left unwritten, errors.
- * In particular every row below seqlens_k[b] must be finite, those of nodes that a token does not see among them.
+ * In particular every row below seqlens_k[b] must be finite, those of nodes that a token does not see among them: NaN
+ * in one reaches lse and max_logits of the tokens that see it, and may reach out of all of the request's.
  * A causal mask (bits 0 .. i) gives the values of the causal form up to the order of its sums.
  */
 smla_status sparse_mla_tree_fwd_paged(const void* q, const void* kv_pool, int64_t pool_rows,

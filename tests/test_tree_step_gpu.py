@@ -365,6 +365,19 @@ def test_tree_broken_queries_stay_visible(bad):
             assert bool(g[broken].isnan().all()) and torch.equal(g[~broken], x[~broken])
 
 
+def test_tree_nan_keys_reach_the_tokens_that_see_them_and_no_other_request():
+    for n_k, heads in ((100, 16), (9000, 128)):
+        w = tree_case(22, [4, 2, 5], [n_k, 90, 300], heads)
+        w["tree_mask"][:4] = i32([[1], [3], [5], [9]])            # the first request: three children of its first node
+        at = n_k - 3                                              # the second node's position
+        w["kv_pool"][w["block_table"][0, at // 64].long() * 64 + at % 64, 0, 7] = float("nan")
+        out, lse, top = smla.sparse_mla_tree_fwd_paged(**w)
+        assert bool(lse[1].isnan().all()) and bool(top[1].isnan().all()) and bool(out[1].isnan().any(-1).all())
+        # its siblings do not see it: their scores and sums are whole, and so is everything of the other requests
+        assert bool(torch.isfinite(lse[[0, 2, 3]]).all()) and bool(torch.isfinite(top[[0, 2, 3]]).all())
+        assert all(bool(torch.isfinite(x[4:].float()).all()) for x in (out, lse, top))
+
+
 def test_tree_refuses_wrong_tensors():
     w = tree_case(18, [2], [70], 16)
     for kw in (dict(tree_mask=w["tree_mask"][:1]), dict(tree_mask=w["tree_mask"][:, 0]), dict(tree_mask=w["tree_mask"].long()),
