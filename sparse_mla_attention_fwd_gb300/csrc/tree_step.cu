@@ -34,10 +34,12 @@ __device__ __forceinline__ NodeRange nodes_of(const int32_t* cu, int64_t b, int6
 // A warp takes a request, 32 nodes at a time, a node a lane.  Within the 32, five rounds of pointer doubling give the
 // set as a word (each round joins the set of the node 2^k steps up); the parent at which a chain leaves the 32 lies in
 // an earlier word, whose row is complete by then.  Latency bounds it: 8 trees of 8 nodes 2.0 us, 300 of 64 2.7 us, 64 of 128
-// 4.1 us, and 2 us for each further 32 nodes of one request (4 trees of 512: 36 us).
+// 4.1 us, and 1.5 to 2 us for each further 32 nodes of one request (4 trees of 512: 23 us).
 constexpr int kPlanWarps = 4;
 constexpr int kPlanMaxCtas = 1216;
-constexpr int kLaneWords = 4;              // rows of up to so many words are written by their node's lane
+// Rows of up to so many words are written by their node's lane, longer ones a word a lane: 4 trees of 512 nodes (16 words) 23 us
+// and 37; a tree of 1024 nodes 67 and 71, a chain of 1024 66 and 37.
+constexpr int kLaneWords = 16;
 constexpr int kMaxPlanNodes = 1 << 30;
 
 struct TreePlanParams {
@@ -579,7 +581,10 @@ __global__ void __launch_bounds__(kVerifyThreads, STEPS == 4 ? 2 : STEPS == 3 ? 
 // CTA 0 does the bookkeeping instead: lengths, and the pages behind them back in front of the free list's start.
 constexpr int kCommitThreads = 256;
 constexpr int kRowsInFlight = 4;
-constexpr int kFewColumns = 4;        // of a request's table, that a thread gives back by itself
+// Columns of a request that a thread gives back by itself, one after the other, more of them a warp: 77 requests of 256 that are done,
+// 20 columns each, 8.5 us and 13; 6 of 32, up to 125 columns, 11.5 and 5 to 6; 6 of 64, up to 1900 columns, 105 and 15.
+constexpr int kFewColumns = 32;
+constexpr int kColumnLoads = 8;       // times 32 columns that a warp looks at at once
 
 struct CommitParams {
   const int32_t* keep;
@@ -622,52 +627,76 @@ __device__ __forceinline__ int64_t columns_of(int64_t len, const CommitParams& p
   return min((len + p.page_block - 1) / p.page_block, static_cast<int64_t>(p.max_blocks));
 }
 
-// Calls put(page, k) for the pages of a request's table columns [first, last), in order, k counting the mapped ones; returns how
-// many there are.  A thread does its own request's few columns by itself; those with more (requests that are done) are done by
-// the warp, one request after the other.
+// Calls put(page, k) for the pages of request b's table columns [first, last), in order, k counting the mapped ones; returns how
+// many there are.  By a thread, or by a warp (in every lane).
 template <typename Put>
-__device__ __forceinline__ int64_t for_pages(const CommitParams& p, int64_t b, int64_t first, int64_t last, Put put) {
+__device__ __forceinline__ int thread_pages(const CommitParams& p, int64_t b, int first, int last, Put put) {
+  int count = 0;
+  for (int col = first; col < last; ++col) {
+    const int32_t page = __ldg(p.block_table + b * p.max_blocks + col);
+    if (page >= 0) put(page, count++);
+  }
+  return count;
+}
+template <typename Put>
+__device__ __forceinline__ int warp_pages(const CommitParams& p, int64_t b, int first, int last, Put put) {
   const int lane = threadIdx.x & 31;
-  int64_t count = 0;
-  const bool few = last - first <= kFewColumns;
-  if (few)
-    for (int64_t col = first; col < last; ++col) {
-      const int32_t page = __ldg(p.block_table + b * p.max_blocks + col);
-      if (page >= 0) put(page, count++, lane);
+  int count = 0;
+  for (int64_t c0 = first; c0 < last; c0 += 32 * kColumnLoads) {
+    int32_t page[kColumnLoads];
+#pragma unroll
+    for (int u = 0; u < kColumnLoads; ++u) {
+      const int64_t col = c0 + 32 * u + lane;
+      page[u] = col < last ? __ldg(p.block_table + b * p.max_blocks + col) : -1;
     }
-  for (uint32_t many = __ballot_sync(kAll, !few); many; many &= many - 1) {
-    const int of = __ffs(many) - 1;
-    const int64_t bo = __shfl_sync(kAll, b, of), c1 = __shfl_sync(kAll, last, of);
-    int64_t found = 0;
-    for (int64_t c0 = __shfl_sync(kAll, first, of); c0 < c1; c0 += 32) {
-      const int32_t page = c0 + lane < c1 ? __ldg(p.block_table + bo * p.max_blocks + c0 + lane) : -1;
-      const uint32_t mapped = __ballot_sync(kAll, page >= 0);
-      if (page >= 0) put(page, found + __popc(mapped & ((1u << lane) - 1u)), of);
-      found += __popc(mapped);
+#pragma unroll
+    for (int u = 0; u < kColumnLoads; ++u) {
+      const uint32_t mapped = __ballot_sync(kAll, page[u] >= 0);
+      if (page[u] >= 0) put(page[u], count + __popc(mapped & ((1u << lane) - 1u)));
+      count += __popc(mapped);
     }
-    if (lane == of) count = found;
   }
   return count;
 }
 
+// A thread a request.  A few columns a thread looks at by itself; requests with more (those that are done) go to the CTA's
+// warps, once to be counted and once to be given back.
 __device__ void commit_lengths(const CommitParams& p) {
-  __shared__ int64_t warp_sum[2][kCommitThreads / 32];
+  constexpr int kWarps = kCommitThreads / 32;
+  __shared__ int64_t warp_sum[2][kWarps];
   __shared__ int64_t place[kCommitThreads];     // of a request's first page, counted down from the list's start
+  __shared__ int cols[2][kCommitThreads], found[kCommitThreads], many[kCommitThreads], n_many;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t start = p.free_pages ? min(max(p.free_start ? static_cast<int64_t>(__ldg(p.free_start)) : p.n_free, int64_t{0}), p.n_free) : 0;
   int64_t pages = 0, tokens = 0;
+  if (tid == 0) n_many = 0;
   for (int64_t b0 = 0; b0 < p.n_req; b0 += kCommitThreads) {
+    __syncthreads();
     const int64_t b = b0 + tid;
     Kept k{0, 0, 0};
-    int64_t first = 0, last = 0;
+    int first = 0, last = 0;
     if (b < p.n_req) {
       k = kept_of(p, b);
       const int64_t len = k.n < 0 ? 0 : max(k.before + k.n, int64_t{0});
       p.seqlens[b] = static_cast<int32_t>(len);
-      first = columns_of(len, p);
-      last = p.free_pages ? columns_of(k.n_k, p) : first;
+      first = static_cast<int>(columns_of(len, p));
+      last = p.free_pages ? static_cast<int>(columns_of(k.n_k, p)) : first;
     }
-    const int64_t back = for_pages(p, b, first, last, [](int32_t, int64_t, int) {});
+    const bool few = last - first <= kFewColumns;
+    if (few) {
+      found[tid] = thread_pages(p, b, first, last, [](int32_t, int) {});
+    } else {
+      cols[0][tid] = first;
+      cols[1][tid] = last;
+      many[atomicAdd(&n_many, 1)] = tid;        // in any order: each has its own place
+    }
+    __syncthreads();
+    for (int i = warp; i < n_many; i += kWarps) {
+      const int of = many[i], n = warp_pages(p, b0 + of, cols[0][of], cols[1][of], [](int32_t, int) {});
+      if (lane == 0) found[of] = n;
+    }
+    __syncthreads();
+    const int64_t back = found[tid];
     int64_t end = back, kept = max(k.n, int64_t{0});
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -683,18 +712,24 @@ __device__ void commit_lengths(const CommitParams& p) {
     }
     __syncthreads();
     int64_t at = pages + end - back;
-    for (int w = 0; w < kCommitThreads / 32; ++w) {
+    for (int w = 0; w < kWarps; ++w) {
       if (w < warp) at += warp_sum[0][w];
       pages += warp_sum[0][w];
       tokens += warp_sum[1][w];
     }
-    place[tid] = at;
-    __syncwarp();
-    for_pages(p, b, first, last, [&](int32_t page, int64_t n, int of) {
-      const int64_t to = start - 1 - (place[32 * warp + of] + n);
+    const auto give_back = [&](int64_t place_of, int32_t page, int n) {
+      const int64_t to = start - 1 - (place_of + n);
       if (to >= 0) p.free_pages[to] = page;
-    });
+    };
+    place[tid] = at;
+    if (few) thread_pages(p, b, first, last, [&](int32_t page, int n) { give_back(at, page, n); });
     __syncthreads();
+    for (int i = warp; i < n_many; i += kWarps) {
+      const int of = many[i];
+      warp_pages(p, b0 + of, cols[0][of], cols[1][of], [&](int32_t page, int n) { give_back(place[of], page, n); });
+    }
+    __syncthreads();
+    if (tid == 0) n_many = 0;
   }
   if (tid == 0) {
     const int64_t given = min(pages, start);
