@@ -198,7 +198,8 @@ __device__ __forceinline__ float left_of(const Residual& r, int v) {
   return fmaxf(x, 0.f);
 }
 
-// A sum in two floats: hi, and in lo what the additions to hi have lost.  64-bit additions run at 2 a clock and SM here.
+// A sum in two floats: hi, and in lo what the additions to hi have lost (Knuth's two-sum).  64-bit additions run at 2 a clock and
+// SM here.
 struct __align__(8) Sum {
   float hi, lo;
   __device__ __forceinline__ void add(float x) {
@@ -411,9 +412,10 @@ __global__ void __launch_bounds__(kVerifyThreads, STEPS == 4 ? 2 : STEPS == 3 ? 
           for (int g = 0; g < n_gone; ++g)
             if (s.gone[g] == x) rx = 0.f;
         }
-        // u q Z < r, the product in two floats
-        const float uq = s.u[k] * s.qx[k], low = fmaf(s.u[k], s.qx[k], -uq);
-        const float h = uq * z.hi, e = fmaf(uq, z.hi, -h) + fmaf(uq, z.lo, low * z.hi);
+        // u q Z < r, the product in two floats.  Products whose rounding is recovered are rounded by name: contracted into
+        // the subtraction behind it, h would not be the number whose error e holds, and the comparison one of 24 bits.
+        const float uq = __fmul_rn(s.u[k], s.qx[k]), low = fmaf(s.u[k], s.qx[k], -uq);
+        const float h = __fmul_rn(uq, z.hi), e = fmaf(uq, z.hi, -h) + fmaf(uq, z.lo, low * z.hi);
         if ((rx - h) - e > 0.f) {
           cur = w0 + k;
           if (lane == 0 && rank == 0) {
@@ -486,7 +488,7 @@ __global__ void __launch_bounds__(kVerifyThreads, STEPS == 4 ? 2 : STEPS == 3 ? 
         summed = true;
       } else if (sum.positive() || (c == 0.f && n_gone == 0)) {
         // the last token lies in the part of the CTA in which the running sum passes u * total
-        const float h = sample_u * sum.hi;
+        const float h = __fmul_rn(sample_u, sum.hi);   // rounded by name, as above
         const Sum target{h, fmaf(sample_u, sum.hi, -h) + sample_u * sum.lo};
         Sum before{0.f, 0.f};
         const int owner = crossing(totals, ranks, target, before);
