@@ -57,6 +57,14 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _int32(value, name):
+    """A size that fits the C interface's 32-bit int; ctypes would wrap a larger one without a word."""
+    value = int(value)
+    if not -_INT32_MAX <= value <= _INT32_MAX:
+        raise ValueError(f"{name} = {value} does not fit the C interface's 32 bits")
+    return value
+
+
 def _stream_handle(stream, device):
     if stream is None:
         stream = torch.cuda.current_stream(device)
@@ -126,6 +134,7 @@ def sparse_mla_fwd_host(q, kv, indices, topk_length=None, attn_sink=None, sm_sca
     out) are allocated here when not given.  The call is asynchronous on `stream`: synchronise
     it before reading the outputs."""
     lib = load_library()
+    d_v, n_chunks = _int32(d_v, "d_v"), _int32(n_chunks, "n_chunks")
     dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
     _host(q, "q", torch.bfloat16)
     _host(kv, "kv", torch.bfloat16)
@@ -134,7 +143,7 @@ def sparse_mla_fwd_host(q, kv, indices, topk_length=None, attn_sink=None, sm_sca
     _host(attn_sink, "attn_sink", torch.float32)
     s_q, h_q, d_qk = q.shape
     s_kv = kv.shape[0]
-    topk = indices.shape[-1]
+    topk = _int32(indices.shape[-1], "topk")
     if sm_scale is None:
         sm_scale = 1.0 / math.sqrt(d_qk)
     if out is None:
@@ -160,10 +169,10 @@ def sparse_mla_fwd_host(q, kv, indices, topk_length=None, attn_sink=None, sm_sca
         copy_streams = (torch.cuda.Stream(dev), torch.cuda.Stream(dev))
     with torch.cuda.device(dev):
         rc = lib.sparse_mla_fwd_host(
-            _ptr(q), _ptr(kv), _ptr(indices), _ptr(topk_length), _ptr(attn_sink), float(sm_scale), int(d_v),
+            _ptr(q), _ptr(kv), _ptr(indices), _ptr(topk_length), _ptr(attn_sink), float(sm_scale), d_v,
             _ptr(out), _ptr(lse), _ptr(max_logits), int(s_q), int(s_kv), int(h_q), int(d_qk), int(topk),
             _ptr(d["q"]), _ptr(d["kv"]), _ptr(d["indices"]), _ptr(d.get("topk_length")), _ptr(d.get("attn_sink")),
-            _ptr(d["out"]), _ptr(d["lse"]), _ptr(d["max_logits"]), int(n_chunks), _stream_handle(stream, dev),
+            _ptr(d["out"]), _ptr(d["lse"]), _ptr(d["max_logits"]), n_chunks, _stream_handle(stream, dev),
             copy_streams[0].cuda_stream, copy_streams[1].cuda_stream)
     if rc != 0:
         raise SmlaError(rc, "sparse_mla_fwd_host")
@@ -221,6 +230,7 @@ def sparse_mla_fwd(q, kv, indices, topk_length=None, attn_sink=None, sm_scale=No
     n_split > 1 (or "auto": see auto_splits) runs the split-KV variant with a workspace
     allocated here."""
     lib = load_library()
+    d_v = _int32(d_v, "d_v")
     _check(q, "q", torch.bfloat16)
     dev = q.device
     _check(kv, "kv", torch.bfloat16, dev)
@@ -231,7 +241,7 @@ def sparse_mla_fwd(q, kv, indices, topk_length=None, attn_sink=None, sm_scale=No
     s_kv = kv.shape[0]
     if kv.numel() != s_kv * d_qk:
         raise ValueError("kv must be [s_kv, 1, d_qk] with the d_qk of q")
-    topk = indices.shape[-1] if indices.dim() else 0
+    topk = _int32(indices.shape[-1], "topk") if indices.dim() else 0
     if indices.numel() != s_q * topk:
         raise ValueError("indices must be [s_q, 1, topk]")
     if topk_length is not None and topk_length.numel() != s_q:
@@ -243,18 +253,19 @@ def sparse_mla_fwd(q, kv, indices, topk_length=None, attn_sink=None, sm_scale=No
     out, lse, max_logits = _outputs(q, h_q, d_v, out, lse, max_logits)
     if n_split == "auto":
         n_split = auto_splits(s_q, h_q, topk, dev)
+    n_split = _int32(n_split, "n_split")
     with torch.cuda.device(dev):
         if n_split == 1:
             rc = lib.sparse_mla_fwd(_ptr(q), _ptr(kv), _ptr(indices), _ptr(topk_length), _ptr(attn_sink),
-                                    float(sm_scale), int(d_v), _ptr(out), _ptr(lse), _ptr(max_logits),
-                                    int(s_q), int(s_kv), int(h_q), int(d_qk), int(topk),
+                                    float(sm_scale), d_v, _ptr(out), _ptr(lse), _ptr(max_logits),
+                                    int(s_q), int(s_kv), int(h_q), int(d_qk), topk,
                                     _stream_handle(stream, dev))
         else:
             ws, nbytes = _workspace(lib, s_q, h_q, n_split, dev)
             rc = lib.sparse_mla_fwd_splitkv(_ptr(q), _ptr(kv), _ptr(indices), _ptr(topk_length),
-                                            _ptr(attn_sink), float(sm_scale), int(d_v), _ptr(out), _ptr(lse),
+                                            _ptr(attn_sink), float(sm_scale), d_v, _ptr(out), _ptr(lse),
                                             _ptr(max_logits), int(s_q), int(s_kv), int(h_q), int(d_qk),
-                                            int(topk), int(n_split), _ptr(ws), int(nbytes),
+                                            topk, n_split, _ptr(ws), int(nbytes),
                                             _stream_handle(stream, dev))
     if rc != 0:
         raise SmlaError(rc, "sparse_mla_fwd")
@@ -269,6 +280,7 @@ def sparse_mla_fwd_paged(q, kv_pool, block_table, indices, page_block=64, seqlen
     max_blocks] int32, seqlens_k [n_req] int32 or None (then every request has s_kv_per_req
     tokens); indices hold token positions within the row's request."""
     lib = load_library()
+    page_block, s_q_per_req, d_v = _int32(page_block, "page_block"), _int32(s_q_per_req, "s_q_per_req"), _int32(d_v, "d_v")
     _check(q, "q", torch.bfloat16)
     dev = q.device
     _check(kv_pool, "kv_pool", torch.bfloat16, dev)
@@ -283,10 +295,10 @@ def sparse_mla_fwd_paged(q, kv_pool, block_table, indices, page_block=64, seqlen
         raise ValueError("kv_pool must be [rows, 1, d_qk] with the d_qk of q")
     if block_table.dim() != 2:
         raise ValueError("block_table must be [n_req, max_blocks]")
-    max_blocks = block_table.shape[1]
+    max_blocks = _int32(block_table.shape[1], "max_blocks")
     if s_kv_per_req is None:
         s_kv_per_req = max_blocks * page_block
-    topk = indices.shape[-1] if indices.dim() else 0
+    topk = _int32(indices.shape[-1], "topk") if indices.dim() else 0
     if indices.numel() != s_q * topk:
         raise ValueError("indices must be [s_q, 1, topk]")
     if sm_scale is None:
@@ -294,21 +306,22 @@ def sparse_mla_fwd_paged(q, kv_pool, block_table, indices, page_block=64, seqlen
     out, lse, max_logits = _outputs(q, h_q, d_v, out, lse, max_logits)
     if n_split == "auto":
         n_split = auto_splits(s_q, h_q, topk, dev)
+    n_split = _int32(n_split, "n_split")
     with torch.cuda.device(dev):
         if n_split == 1:
             rc = lib.sparse_mla_fwd_paged(_ptr(q), _ptr(kv_pool), int(pool_rows), _ptr(block_table),
-                                          int(max_blocks), int(page_block), _ptr(seqlens_k),
-                                          int(s_kv_per_req), int(s_q_per_req), _ptr(indices),
-                                          _ptr(topk_length), _ptr(attn_sink), float(sm_scale), int(d_v),
+                                          max_blocks, page_block, _ptr(seqlens_k),
+                                          int(s_kv_per_req), s_q_per_req, _ptr(indices),
+                                          _ptr(topk_length), _ptr(attn_sink), float(sm_scale), d_v,
                                           _ptr(out), _ptr(lse), _ptr(max_logits), int(s_q), int(h_q),
-                                          int(d_qk), int(topk), _stream_handle(stream, dev))
+                                          int(d_qk), topk, _stream_handle(stream, dev))
         else:
             ws, nbytes = _workspace(lib, s_q, h_q, n_split, dev)
             rc = lib.sparse_mla_fwd_paged_splitkv(
-                _ptr(q), _ptr(kv_pool), int(pool_rows), _ptr(block_table), int(max_blocks), int(page_block),
-                _ptr(seqlens_k), int(s_kv_per_req), int(s_q_per_req), _ptr(indices), _ptr(topk_length),
-                _ptr(attn_sink), float(sm_scale), int(d_v), _ptr(out), _ptr(lse), _ptr(max_logits), int(s_q),
-                int(h_q), int(d_qk), int(topk), int(n_split), _ptr(ws), int(nbytes), _stream_handle(stream, dev))
+                _ptr(q), _ptr(kv_pool), int(pool_rows), _ptr(block_table), max_blocks, page_block,
+                _ptr(seqlens_k), int(s_kv_per_req), s_q_per_req, _ptr(indices), _ptr(topk_length),
+                _ptr(attn_sink), float(sm_scale), d_v, _ptr(out), _ptr(lse), _ptr(max_logits), int(s_q),
+                int(h_q), int(d_qk), topk, n_split, _ptr(ws), int(nbytes), _stream_handle(stream, dev))
     if rc != 0:
         raise SmlaError(rc, "sparse_mla_fwd_paged")
     return out, lse, max_logits
@@ -322,6 +335,8 @@ def sparse_mla_fwd_paged_splitkv_static(q, kv_pool, block_table, indices, n_spli
     (no workspace is allocated anywhere).  Calls on one device must not overlap; see the C
     header."""
     lib = load_library()
+    page_block, s_q_per_req, d_v = _int32(page_block, "page_block"), _int32(s_q_per_req, "s_q_per_req"), _int32(d_v, "d_v")
+    n_split = _int32(n_split, "n_split")
     _check(q, "q", torch.bfloat16)
     dev = q.device
     _check(kv_pool, "kv_pool", torch.bfloat16, dev)
@@ -332,19 +347,19 @@ def sparse_mla_fwd_paged_splitkv_static(q, kv_pool, block_table, indices, n_spli
     _check(attn_sink, "attn_sink", torch.float32, dev)
     s_q, h_q, d_qk = q.shape
     pool_rows = kv_pool.shape[0]
-    max_blocks = block_table.shape[1]
+    max_blocks = _int32(block_table.shape[1], "max_blocks")
     if s_kv_per_req is None:
         s_kv_per_req = max_blocks * page_block
-    topk = indices.shape[-1] if indices.dim() else 0
+    topk = _int32(indices.shape[-1], "topk") if indices.dim() else 0
     if sm_scale is None:
         sm_scale = 1.0 / math.sqrt(d_qk)
     out, lse, max_logits = _outputs(q, h_q, d_v, out, lse, max_logits)
     with torch.cuda.device(dev):
         rc = lib.sparse_mla_fwd_paged_splitkv_static(
-            _ptr(q), _ptr(kv_pool), int(pool_rows), _ptr(block_table), int(max_blocks), int(page_block),
-            _ptr(seqlens_k), int(s_kv_per_req), int(s_q_per_req), _ptr(indices), _ptr(topk_length),
-            _ptr(attn_sink), float(sm_scale), int(d_v), _ptr(out), _ptr(lse), _ptr(max_logits), int(s_q),
-            int(h_q), int(d_qk), int(topk), int(n_split), _stream_handle(stream, dev))
+            _ptr(q), _ptr(kv_pool), int(pool_rows), _ptr(block_table), max_blocks, page_block,
+            _ptr(seqlens_k), int(s_kv_per_req), s_q_per_req, _ptr(indices), _ptr(topk_length),
+            _ptr(attn_sink), float(sm_scale), d_v, _ptr(out), _ptr(lse), _ptr(max_logits), int(s_q),
+            int(h_q), int(d_qk), topk, n_split, _stream_handle(stream, dev))
     if rc != 0:
         raise SmlaError(rc, "sparse_mla_fwd_paged_splitkv_static")
     return out, lse, max_logits
@@ -357,6 +372,7 @@ def sparse_mla_bwd(q, kv, out, dout, indices, lse, topk_length=None, attn_sink=N
     fp32 as it returned them; dout [s_q, h_q, d_v] bf16.  Returns (dq [s_q, h_q, d_qk] fp32,
     dkv [s_kv, d_qk] fp32, dsink [h_q] fp32 or None)."""
     lib = load_library()
+    d_v = _int32(d_v, "d_v")
     _check(q, "q", torch.bfloat16)
     dev = q.device
     _check(kv, "kv", torch.bfloat16, dev)
@@ -370,7 +386,7 @@ def sparse_mla_bwd(q, kv, out, dout, indices, lse, topk_length=None, attn_sink=N
     s_kv = kv.shape[0]
     if kv.numel() != s_kv * d_qk:
         raise ValueError("kv must be [s_kv, 1, d_qk] with the d_qk of q")
-    topk = indices.shape[-1] if indices.dim() else 0
+    topk = _int32(indices.shape[-1], "topk") if indices.dim() else 0
     if indices.numel() != s_q * topk:
         raise ValueError("indices must be [s_q, 1, topk]")
     if out.numel() != s_q * h_q * d_v or dout.numel() != s_q * h_q * d_v or lse.numel() != s_q * h_q:
@@ -392,8 +408,8 @@ def sparse_mla_bwd(q, kv, out, dout, indices, lse, topk_length=None, attn_sink=N
     _check(dsink, "dsink", torch.float32, dev)
     with torch.cuda.device(dev):
         rc = lib.sparse_mla_bwd(_ptr(q), _ptr(kv), _ptr(out), _ptr(dout), _ptr(indices), _ptr(topk_length),
-                                _ptr(attn_sink), _ptr(lse), float(sm_scale), int(d_v), _ptr(dq), _ptr(dkv),
-                                _ptr(dsink), int(s_q), int(s_kv), int(h_q), int(d_qk), int(topk),
+                                _ptr(attn_sink), _ptr(lse), float(sm_scale), d_v, _ptr(dq), _ptr(dkv),
+                                _ptr(dsink), int(s_q), int(s_kv), int(h_q), int(d_qk), topk,
                                 _stream_handle(stream, dev))
     if rc != 0:
         raise SmlaError(rc, "sparse_mla_bwd")
@@ -476,6 +492,7 @@ def sparse_mla_plan_pages(seqlens, new_lens, block_table, free_pages, n_tokens, 
     pages that were missing.  See the C header for the exact rules."""
     lib = load_library()
     i32 = torch.int32
+    page_block = _int32(page_block, "page_block")
     dev = _dense(seqlens, "seqlens", i32)
     if stream is not None or torch.cuda.current_device() != dev.index:
         return _on_device(sparse_mla_plan_pages, dev, stream, seqlens, new_lens, block_table, free_pages, n_tokens, page_block,
@@ -501,7 +518,7 @@ def sparse_mla_plan_pages(seqlens, new_lens, block_table, free_pages, n_tokens, 
     rc = lib.sparse_mla_plan_pages(
         seqlens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(), _ptr(free_start),
         k.data_ptr(), cu.data_ptr(), sl.data_ptr(), pos.data_ptr(), cnt.data_ptr(), n_req, free_pages.numel(), n_tokens,
-        table_shape[1], int(page_block), _raw_stream(dev.index))
+        _int32(table_shape[1], "max_blocks"), page_block, _raw_stream(dev.index))
     if rc != 0:
         raise SmlaError(rc, "sparse_mla_plan_pages")
     return k, cu, sl, pos, cnt
@@ -600,7 +617,7 @@ def _dense_attention_args(index, q, kv_pool, block_table, cu_seqlens_q, seqlens_
         raise ValueError("kv_pool must be [rows, 1, d_qk] with the d_qk of q")
     if len(table_shape) != 2:
         raise ValueError("block_table must be [n_req, max_blocks]")
-    n_req, max_blocks = table_shape
+    n_req, max_blocks = table_shape[0], _int32(table_shape[1], "max_blocks")
     if seqlens_k.numel() != n_req or cu_seqlens_q.numel() != n_req + 1:
         raise ValueError("seqlens_k must have n_req entries and cu_seqlens_q n_req + 1")
     if attn_sink is not None:
@@ -636,6 +653,7 @@ def sparse_mla_chunk_fwd_paged(q, kv_pool, block_table, cu_seqlens_q, seqlens_k,
     sparse_mla_chunk_workspace_size bytes, 256-byte aligned) is allocated here when not given; calls
     that may overlap must not share one."""
     lib = load_library()
+    page_block, d_v = _int32(page_block, "page_block"), _int32(d_v, "d_v")
     index = _here(q, stream)
     if index < 0:
         dev = _dense(q, "q", torch.bfloat16)
@@ -644,8 +662,8 @@ def sparse_mla_chunk_fwd_paged(q, kv_pool, block_table, cu_seqlens_q, seqlens_k,
     n_tok, h_q, d_qk, pool_rows, n_req, max_blocks, out, lse, max_logits, sm_scale, workspace, ws_bytes = _dense_attention_args(
         index, q, kv_pool, block_table, cu_seqlens_q, seqlens_k, attn_sink, sm_scale, d_v, out, lse, max_logits, workspace, lib)
     rc = lib.sparse_mla_chunk_fwd_paged(
-        q.data_ptr(), kv_pool.data_ptr(), pool_rows, block_table.data_ptr(), max_blocks, int(page_block),
-        cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), n_req, 1 if causal else 0, _ptr(attn_sink), float(sm_scale), int(d_v),
+        q.data_ptr(), kv_pool.data_ptr(), pool_rows, block_table.data_ptr(), max_blocks, page_block,
+        cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), n_req, 1 if causal else 0, _ptr(attn_sink), float(sm_scale), d_v,
         out.data_ptr(), lse.data_ptr(), max_logits.data_ptr(), n_tok, h_q, d_qk, workspace.data_ptr(), ws_bytes,
         _raw_stream(index))
     if rc != 0:
@@ -696,6 +714,7 @@ def sparse_mla_tree_fwd_paged(q, kv_pool, block_table, cu_seqlens_q, seqlens_k, 
     :func:`sparse_mla_plan_tree`; any mask will do).  Everything else, workspace and returned values among it, is as
     there."""
     lib = load_library()
+    page_block, d_v = _int32(page_block, "page_block"), _int32(d_v, "d_v")
     index = _here(q, stream)
     if index < 0:
         dev = _dense(q, "q", torch.bfloat16)
@@ -709,9 +728,9 @@ def sparse_mla_tree_fwd_paged(q, kv_pool, block_table, cu_seqlens_q, seqlens_k, 
     if len(mask_shape) != 2 or mask_shape[0] != n_tok or not 0 < mask_shape[1] <= 1024:
         raise ValueError("tree_mask must be [n_tok, words], 1 to 1024 words")
     rc = lib.sparse_mla_tree_fwd_paged(
-        q.data_ptr(), kv_pool.data_ptr(), pool_rows, block_table.data_ptr(), max_blocks, int(page_block),
+        q.data_ptr(), kv_pool.data_ptr(), pool_rows, block_table.data_ptr(), max_blocks, page_block,
         cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), n_req, tree_mask.data_ptr(), mask_shape[1], _ptr(attn_sink),
-        float(sm_scale), int(d_v), out.data_ptr(), lse.data_ptr(), max_logits.data_ptr(), n_tok, h_q, d_qk,
+        float(sm_scale), d_v, out.data_ptr(), lse.data_ptr(), max_logits.data_ptr(), n_tok, h_q, d_qk,
         workspace.data_ptr(), ws_bytes, _raw_stream(index))
     if rc != 0:
         raise SmlaError(rc, "sparse_mla_tree_fwd_paged")
@@ -817,6 +836,7 @@ def sparse_mla_commit_tree(keep, n_keep, cu_seqlens_q, seqlens_k, block_table, k
     per layer and give free_pages in one of the calls."""
     lib = load_library()
     i32 = torch.int32
+    page_block = _int32(page_block, "page_block")
     index = _here(keep, stream)
     if index < 0:
         dev = _dense(keep, "keep", i32)
@@ -850,8 +870,8 @@ def sparse_mla_commit_tree(keep, n_keep, cu_seqlens_q, seqlens_k, block_table, k
     counts = _empty_strided((3,), (1,), i32) if counts is None else _int_output(counts, "counts", 3, keep.device)
     rc = lib.sparse_mla_commit_tree(
         keep.data_ptr(), n_keep.data_ptr(), keep_shape[1], cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), block_table.data_ptr(),
-        table_shape[1], int(page_block), n_req, pool, layers, layer_stride, pool_rows, d_qk, free, n_free, _ptr(free_start),
-        seqlens.data_ptr(), counts.data_ptr(), _raw_stream(index))
+        _int32(table_shape[1], "max_blocks"), page_block, n_req, pool, _int32(layers, "layers"), layer_stride, pool_rows, d_qk, free,
+        n_free, _ptr(free_start), seqlens.data_ptr(), counts.data_ptr(), _raw_stream(index))
     if rc != 0:
         raise SmlaError(rc, "sparse_mla_commit_tree")
     return seqlens, counts
