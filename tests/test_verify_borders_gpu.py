@@ -110,3 +110,44 @@ def test_last_tokens_next_to_the_border(vocab, n_req, times, draft):
     w["accept_u"].copy_(torch.from_numpy(u.reshape(-1)))
     w["sample_u"].copy_(torch.from_numpy(s))
     assert bool((verify_check(w)[2] == 1).all())
+
+
+@pytest.mark.parametrize("times", [1, 2, 4])
+@pytest.mark.parametrize("vocab,n_req", [(50, 2000), (9001, 150)])
+def test_residuals_against_the_rule_without_roundings(vocab, n_req, times):
+    """r and C are rounded to fp32.  Against the rule in 64 bits throughout: C is off by its own rounding, 2^-24 of it, and by Z's
+    error; r(v) by q(v) times that and its own rounding; Z by the sum of r's.  Where the decision's margin is larger, it is the same."""
+    w, tokens, u, _, _, _ = rejected(51 + times, n_req, vocab, True, times)
+    nodes, rng, every, half = times + 2, np.random.default_rng(vocab + times), np.arange(n_req), 2.0 ** -24
+    p, q = rows_of(w, "target_probs")[::nodes], rows_of(w, "draft_probs")[::nodes]
+
+    def exact(rejections):
+        C, Z, off_c, off_z = np.zeros(n_req), np.ones(n_req), np.zeros(n_req), np.zeros(n_req)
+        for k in range(rejections):
+            C = C + Z
+            off_c = off_c + off_z + (half * C if k else 0)         # the first sum is 1, which has no rounding
+            r = np.maximum(p - C[:, None] * q, 0)
+            Z = r.sum(1)
+            off_z = off_c * q.sum(1) + half * Z
+        return r, Z, off_c, off_z
+
+    r, Z, off_c, off_z = exact(times)
+    x, last = tokens[:, -1], rng.random(n_req).astype(np.float32)
+    u[:, -1] = last
+    left, need = last * q[every, x] * Z, r[every, x]
+    clear = np.abs(left - need) > 1.01 * (last * q[every, x] * off_z + off_c * q[every, x] + half * need)
+    clear |= (need == 0) & (p[every, x] < 0.99 * q[every, x])      # 0 with and without roundings
+    kept = left < need
+    r, Z, off_c, off_z = exact(times + 1)
+    s = rng.random(n_req).astype(np.float32)
+    sums = r.cumsum(1)
+    drawn = (sums > (s * Z)[:, None]).argmax(1)
+    sure = clear & (np.abs(sums - (s * Z)[:, None]).min(1) > 1.01 * (1 + s) * off_z)
+    w["tokens"].copy_(torch.from_numpy(tokens.reshape(-1)))
+    w["accept_u"].copy_(torch.from_numpy(u.reshape(-1)))
+    w["sample_u"].copy_(torch.from_numpy(s))
+    _, out, n_keep = (t.cpu().numpy() for t in verify_check(w))
+    assert clear.mean() > 0.9 and sure.mean() > 0.3 and 0 < kept.sum() < n_req
+    assert np.array_equal(n_keep[clear], 1 + kept[clear])
+    again = sure & ~kept
+    assert np.array_equal(out[again, 0], drawn[again])
