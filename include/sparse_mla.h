@@ -346,7 +346,8 @@ smla_status sparse_mla_append_kv_counted(const void* c_kv, int64_t c_stride, con
  * and the row is < pool_rows; any other is an invalid slot and never an address.  Rows of
  * positions at or past seqlens_k[b] are not read into any product: they may hold anything, NaN
  * among it.  Rows below it must be finite: NaN in one reaches every token that sees it, and may reach
- * the request's others.  A (token, head) row of q with NaN in it gives NaN in that row's out, lse and
+ * the request's others.  Scores and softmax sums are fp32; the softmax weights are rounded to bf16, the type of V, before their
+ * product with V (2^-8 of a weight at most; lse and max_logits take the unrounded ones), and out once.  A (token, head) row of q with NaN in it gives NaN in that row's out, lse and
  * max_logits and in no other's, and a score above fp32's range NaN in that row's out and lse.  One below
  * it (-inf) counts as a masked one.
  *   h_q           1 .. 1024 (any: all heads of a token share the one latent row)
@@ -432,7 +433,8 @@ smla_status sparse_mla_tree_fwd_paged(const void* q, const void* kv_pool, int64_
  * When no child is left, or max_keep nodes are kept, the request's last token is drawn from the current r: the first v
  * with r(0) + .. + r(v) > sample_u[b] * sum r (the last v with r(v) > 0 where rounding leaves none; with r all zero,
  * p's; -1 when p has no positive value).  The tokens kept and drawn follow the target's distribution, whatever the
- * drafts.  Products, sums of r, Z and the comparisons hold 46 bits and more, in an order that depends on the sizes alone.
+ * drafts.  Products (of 2^-100 and more), sums of r, Z and the comparisons hold 46 bits and more, in an order that depends on the
+ * sizes alone.
  *   target_probs [n_tok, vocab] fp32, vocab 1 .. 2^30, row stride target_stride elements (>= vocab); rows sum to 1; NaN and negative
  *                values count as 0
  *   draft_probs  [n_tok, vocab] fp32, row stride draft_stride, or NULL; row t is what node t's children were drawn
@@ -462,7 +464,10 @@ smla_status sparse_mla_verify_tree(const float* target_probs, int64_t target_str
  * n_keep[b] < 0 ends the request: no row moves, seqlens[b] = 0 and all of its pages go back.
  *   keep         [n_req, max_keep] int32, n_keep [n_req] int32: as sparse_mla_verify_tree writes them.  A request's
  *                entries ascend and are below n_b; where they do not, its rows from before on are undefined.
- *   seqlens_k    [n_req], cu_seqlens_q [n_req + 1], block_table [n_req, max_blocks]: as in the attention.  The table
+ *   seqlens_k    [n_req], cu_seqlens_q [n_req + 1], block_table [n_req, max_blocks]: those of the attention, but the sums are taken as
+ *                they are, since no n_tok is known here: 0 <= cu_seqlens_q[b] <= cu_seqlens_q[b + 1] <= n_tok of the step's other
+ *                calls, as sparse_mla_plan_pages writes them.  (Those clamp sums to n_tok; with sums past it they would take the
+ *                first new position to be another than this call does, and other rows would be moved.)  The table
  *                is not changed: entries behind the new length are stale, and sparse_mla_plan_pages writes over them.
  *                A row without a page is neither moved nor written.
  *   kv_pool      [n_layers, pool_rows, d_qk] bf16, layers layer_stride elements apart (a multiple of 8, at least

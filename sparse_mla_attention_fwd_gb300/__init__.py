@@ -649,7 +649,8 @@ def sparse_mla_chunk_fwd_paged(q, kv_pool, block_table, cu_seqlens_q, seqlens_k,
     kv_pool, block_table and page_block as for :func:`sparse_mla_fwd_paged`; seqlens_k [n_req] int32
     counts the cached keys with the new tokens' own; causal: a token sees the positions up to its
     own, else every key.  Returns (out [n_tok, h, d_v] bf16, lse [n_tok, h] fp32, max_logits [n_tok,
-    h] fp32); rows of no request are not written.  `workspace` (uint8, at least
+    h] fp32); rows of no request are not written.  Sums are fp32; softmax weights are rounded to bf16 before their product with
+    the values, the output once more.  `workspace` (uint8, at least
     sparse_mla_chunk_workspace_size bytes, 256-byte aligned) is allocated here when not given; calls
     that may overlap must not share one."""
     lib = load_library()
@@ -761,7 +762,7 @@ def sparse_mla_verify_tree(target_probs, tokens, parents, cu_seqlens_q, accept_u
     chosen outright.  Both may be strided over rows.  Returns int32 tensors (allocated here when not given): keep
     [n_req, max_keep], node 0 and the nodes kept behind it (for :func:`sparse_mla_commit_tree`); out_tokens [n_req,
     max_keep], their tokens but the first one's and the token drawn in the end; n_keep [n_req], how many.  The tokens
-    follow the target's distribution.  See the C header for the exact rules."""
+    follow the target's distribution.  Nodes of a request from 1024 on are not tried.  See the C header for the exact rules."""
     lib = load_library()
     i32, f32 = torch.int32, torch.float32
     index = _here(tokens, stream)
@@ -832,7 +833,8 @@ def sparse_mla_commit_tree(keep, n_keep, cu_seqlens_q, seqlens_k, block_table, k
     new lengths go back into free_pages [n_free] int32 in front of index free_start [1] (int32; None: n_free).  A
     request with n_keep[b] < 0 is done: its length becomes 0 and all its pages go back.  Returns int32 tensors (allocated
     here when not given): seqlens [n_req], and counts [3] = tokens kept, next free_start, pages without room;
-    both go into the next :func:`sparse_mla_plan_pages`.  block_table is not changed.  With a tensor per layer, call once
+    both go into the next :func:`sparse_mla_plan_pages`.  cu_seqlens_q is taken as it is (the step's other calls clamp it to their
+    token count): its last entry must not pass theirs.  block_table is not changed.  With a tensor per layer, call once
     per layer and give free_pages in one of the calls."""
     lib = load_library()
     i32 = torch.int32

@@ -149,11 +149,11 @@ __global__ void __launch_bounds__(32 * kPlanWarps) plan_tree_kernel(const TreePl
 // memory.  All CTAs walk the tree alike; they exchange their sums only (one cluster barrier a pass).  The last token's place
 // is narrowed down from the CTAs' sums to a tile's and to four values a thread, so a row is read once a pass.
 //
-// What bounds it.  Large batches: DRAM.  256 chains of up to six nodes over 128000 tokens, 236 MB: 45 us, of which 37 us are
+// What bounds it.  Large batches: DRAM.  256 chains of 3 to 6 nodes over 128000 tokens, 236 MB: 45.5 us, of which 37 us are
 // the rows (6.4 TB/s; 6.7 TB/s by the difference of two vocabularies) and 8 us the chain of latencies in front (sums of nodes,
-// nodes, their probabilities, the walk) and behind (exchange, search).  Small ones: that chain, 5.8 us for a request of one
+// nodes, their probabilities, the walk) and behind (exchange, search).  Small ones: that chain, 5.5 us for a request of one
 // node and 32000 tokens, and 2 to 3 us for each further pass (32 trees with up to five rejections at a node over 100003
-// tokens: 19 us).  The first form, one CTA a request and 64-bit sums: 1 chain 25 us, 256 chains 162, 32 trees 203.  No faster:
+// tokens: 19 to 20 us).  The first form, one CTA a request and 64-bit sums: 1 chain 25 us, 256 chains 162, 32 trees 203.  No faster:
 // 16 CTAs a cluster, copies through shared memory (cp.async, 4 bytes), CTAs of 512 or 1024 threads, the warps' sums sent
 // without the CTA's.
 constexpr int kVerifyThreads = 256;
@@ -164,6 +164,7 @@ constexpr int kMaxNodes = 1024;       // of a request; further ones are not test
 constexpr int kWindow = 256;          // nodes in shared memory at a time
 constexpr int kMaxTiles = 256;        // of a CTA
 constexpr int kTile = 4 * kVerifyThreads;   // values of a tile at most, where kMaxTiles of them are enough
+constexpr int kSms = 152;             // a GB300's; the launch is fitted to them, and no result depends on it
 
 struct VerifyParams {
   const float* target;
@@ -583,8 +584,9 @@ __global__ void __launch_bounds__(kVerifyThreads, STEPS == 4 ? 2 : STEPS == 3 ? 
 // CTA 0 does the bookkeeping instead: lengths, and the pages behind them back in front of the free list's start.
 constexpr int kCommitThreads = 256;
 constexpr int kRowsInFlight = 4;
-// Columns of a request that a thread gives back by itself, one after the other, more of them a warp: 77 requests of 256 that are done,
-// 20 columns each, 8.5 us and 13; 6 of 32, up to 125 columns, 11.5 and 5 to 6; 6 of 64, up to 1900 columns, 105 and 15.
+// Columns of a request that a thread gives back by itself, one after the other, more of them a warp.  By threads alone, by warps alone,
+// and by this rule: 86 requests of 256 that are done, up to 38 columns, 21 on average, 6.5, 16.9 and 7.9 us; 7 of 32, up to 92 columns,
+// 9.6, 4.1 and 5.5; 11 of 64, up to 1631 columns, 115, 14.1 and 13.5.
 constexpr int kFewColumns = 32;
 constexpr int kColumnLoads = 8;       // times 32 columns that a warp looks at at once
 
@@ -847,19 +849,21 @@ smla_status sparse_mla_verify_tree(const float* target_probs, int64_t target_str
   VerifyParams p{target_probs, draft_probs, tokens, parents, cu_seqlens_q, accept_u, sample_u, keep, out_tokens,
                  n_keep, target_stride, draft_stride, n_req, n_tok, vocab, max_keep, 0, 0};
   // CTAs a request, and steps of loads under way: four where two CTAs an SM are enough, three for three, two for four.  Clusters of
-  // four and more do not fill the GPU to the last place, and what does not fit runs after the rest.  Over 128000 tokens, in us,
-  // (CTAs, steps): 48 requests 11.7 (8, 3), 12.6 (8, 2), 12.8 (4, 4); 76 requests 20 (4, 2), 21 (2, 4), 24 (4, 4), which just does not
-  // fit; 128 requests 26.0 (2, 4), 26.1 (4, 2); 152 requests 28 (2, 4), 34 (2, 2), 38 (4, 2); 200 requests 33 (2, 3), 36 (2, 2), 38 (1, 4);
-  // 256 requests 41.6 (1, 4), 42.0 (2, 2), 45 (1, 3), 54 (1, 2); 400 requests 59 (1, 3), 63 (1, 2), 74 (1, 4); 512 requests 72 (1, 2),
-  // 79 (1, 4), 93 (1, 3).  One request over 32000 tokens 6.7 (8), 7.4 (4), 8.5 (2), 10.8 (1).
+  // four and more do not fill the GPU to the last place (they fall 16 or 64 short, found by trial), and what does not fit runs after
+  // the rest.  Chains of 3 to 6 nodes with the draft's rows over 128000 tokens, in us, (CTAs, steps), the chosen pair first:
+  // 48 requests 13.8 (8, 3), 14.5 (8, 2), 14.8 (4, 4); 76 requests 20.0 (4, 3), 21.3 (4, 2), 22.2 (2, 4), 27.1 (4, 4), which just does
+  // not fit; 128 requests 27.0 (2, 4), 26.8 (4, 2); 152 requests 30.5 (2, 4), 31.6 (2, 3), 34.6 (2, 2), 41.3 (4, 2); 200 requests
+  // 38.3 (2, 3), 39.8 (2, 2), 40.6 (1, 4); 256 requests 45.5 (1, 4), 45.9 (2, 2), 48.1 (1, 3), 56.2 (1, 2); 400 requests 65.1 (1, 3),
+  // 68.0 (1, 2), 80.1 (1, 4); 512 requests 80.4 (1, 2), 87.0 (1, 4), 100.3 (1, 3).  One request of one node over 32000 tokens
+  // 5.5 (8, 4), 5.9 (4, 4), 6.9 (2, 4), 8.4 (1, 4).
   const auto fits = [&](int r, int steps) {
-    return r * n_req <= 152 * (steps == 4 ? 2 : steps == 3 ? 3 : 4) - (r < 4 ? 0 : r == 4 || steps == 4 ? 16 : 64);
+    return r * n_req <= kSms * (steps == 4 ? 2 : steps == 3 ? 3 : 4) - (r < 4 ? 0 : r == 4 || steps == 4 ? 16 : 64);
   };
   const auto room = [&](int r) { return r < kMaxCluster && vocab > r * kTile; };
   int ranks = 1, steps = fits(1, 4) ? 4 : fits(1, 3) ? 3 : 2;
   if (steps == 4) {
     while (room(ranks) && fits(2 * ranks, 4)) ranks *= 2;
-    if (room(ranks) && ranks * n_req <= 3 * 152 / 2) {
+    if (room(ranks) && ranks * n_req <= 3 * kSms / 2) {
       ranks *= 2;
       steps = fits(ranks, 3) ? 3 : 2;
     }
