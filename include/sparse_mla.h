@@ -346,10 +346,11 @@ smla_status sparse_mla_append_kv_counted(const void* c_kv, int64_t c_stride, con
  * and the row is < pool_rows; any other is an invalid slot and never an address.  Rows of
  * positions at or past seqlens_k[b] are not read into any product: they may hold anything, NaN
  * among it.  Rows below it must be finite: NaN in one reaches every token that sees it, and may reach
- * the request's others.  Scores and softmax sums are fp32; the softmax weights are rounded to bf16, the type of V, before their
- * product with V (2^-8 of a weight at most; lse and max_logits take the unrounded ones), and out once.  A (token, head) row of q with NaN in it gives NaN in that row's out, lse and
+ * the request's others.  A (token, head) row of q with NaN in it gives NaN in that row's out, lse and
  * max_logits and in no other's, and a score above fp32's range NaN in that row's out and lse.  One below
  * it (-inf) counts as a masked one.
+ * Scores and softmax sums are fp32.  The softmax weights are rounded to bf16, the type of V, before their product
+ * with V (2^-8 of a weight at most; lse and max_logits take the unrounded ones), and out once more.
  *   h_q           1 .. 1024 (any: all heads of a token share the one latent row)
  *   n_tok * h_q   at most INT32_MAX
  *   workspace     device buffer of at least sparse_mla_chunk_workspace_size(n_tok, h_q) bytes,
